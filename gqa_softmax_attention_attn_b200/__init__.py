@@ -19,12 +19,19 @@ from ._native import (  # noqa: F401
     attn_sink_decode_noalloc,
     attn_sink_decode_paged,
     attn_sink_decode_paged_workspace_size,
+    attn_sink_decode_tree,
+    attn_sink_decode_tree_paged,
+    attn_sink_decode_tree_workspace_size,
     attn_sink_decode_workspace_size,
     attn_sink_fwd,
     attn_sink_fwd_host,
     attn_sink_fwd_host_workspace_size,
     attn_sink_fwd_varlen,
     attn_sink_get_device_status,
+    attn_sink_page_map,
+    attn_sink_qk_norm_prologue,
+    attn_sink_qk_norm_prologue_bwd,
+    attn_sink_qk_norm_prologue_bwd_workspace_size,
     attn_sink_qkv_prologue,
     attn_sink_set_wait_timeout_ns,
     attn_sink_version,

@@ -171,6 +171,99 @@ DecodeShape decode_shape_paged(int B, int max_pages, int page_size, int num_page
     return s;
 }
 
+// The work of one CTA of the tree decode spans `rows` rows (a KV head's query
+// heads times the sequence's tokens, at most a row tile) and one chunk of keys.
+TreeShape tree_shape(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, int D, int window, float scale,
+                     int num_splits, int dtype)
+{
+    TreeShape s{};
+    s.B = B;
+    s.total_q = total_q;
+    s.max_q = max_q;
+    s.Lmax = Lmax;
+    s.Hq = Hq;
+    s.Hkv = Hkv;
+    s.D = D;
+    s.window = window;
+    s.scale = scale;
+    const int tile = dtype == ATTN_SINK_DTYPE_F32 ? 16 : 128;
+    const long long all_rows = (long long)max_q * (Hq / Hkv);
+    const long long ctas = (long long)B * Hkv * ((all_rows + tile - 1) / tile);
+    // keys from the first one a root sees, rounded down to a tile, to the last drafted one
+    const long long lw = window > 0 ? (long long)window - 1 + max_q + kTreeTile - 1 : (long long)Lmax;
+    const long long lvis = lw < Lmax ? lw : Lmax;
+    long long splits = num_splits;
+    long long least = kTreeTile;
+    if (splits == 0) {
+        splits = (B == 1 ? 1 : 16) * 296 / ctas;
+        const long long rows = all_rows < tile ? all_rows : tile;
+        least = 16 * rows > 256 ? 16 * rows : 256;
+    }
+    splits = splits < 1 ? 1 : (splits > kTreeMaxSplits ? kTreeMaxSplits : splits);
+    long long chunk = (lvis + splits - 1) / splits;
+    chunk = ((chunk > least ? chunk : least) + kTreeTile - 1) / kTreeTile * kTreeTile;
+    s.chunk = (int)(chunk < 0x7fffffc0LL ? chunk : 0x7fffffc0LL);
+    s.splits = (int)((lvis + s.chunk - 1) / s.chunk);
+    return s;
+}
+
+int check_tree(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, int D, int num_splits, int dtype)
+{
+    const int rc = check_common(B, total_q, Lmax, Hq, Hkv, D, dtype);
+    if (rc != ATTN_SINK_OK) return rc;
+    if (max_q <= 0 || num_splits < 0 || num_splits > kTreeMaxSplits) return ATTN_SINK_ERR_INVALID_ARG;
+    return max_q > kTreeMaxTokens ? ATTN_SINK_ERR_UNSUPPORTED : ATTN_SINK_OK;
+}
+
+size_t tree_ws_bytes(const TreeShape &s)
+{
+    return s.splits <= 1 ? 0 : (size_t)s.total_q * s.Hq * s.splits * (s.D + 2) * sizeof(float);
+}
+
+// both cache layouts, once the sizes are checked
+int run_tree(const void *q, const void *kc, const void *vc, void *out, float *lse, TreeShape &s, void *workspace,
+             size_t ws_bytes, int dtype, void *stream)
+{
+    if (dtype == ATTN_SINK_DTYPE_BF16 && !(s.scale > 0.f && s.scale < INFINITY)) return ATTN_SINK_ERR_UNSUPPORTED;
+    const void *ptrs[] = {q, kc, vc, out, lse, s.page_table, s.cu_q, s.parents, s.seqlens, s.sinks};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return ATTN_SINK_ERR_MISALIGNED;
+    const size_t need = tree_ws_bytes(s);
+    if (need > 0 && (!workspace || ws_bytes < need)) return ATTN_SINK_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return ATTN_SINK_ERR_MISALIGNED;
+    const int rc = ensure_device();
+    if (rc != ATTN_SINK_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    float *ws_o = static_cast<float *>(workspace);
+    float *ws_ml = need > 0 ? ws_o + (size_t)s.total_q * s.Hq * s.splits * s.D : nullptr;
+    using bf = __nv_bfloat16;
+    cudaError_t e;
+    if (dtype == ATTN_SINK_DTYPE_F32) {
+        e = launch_tree_simt<float>(static_cast<const float *>(q), static_cast<const float *>(kc),
+                                    static_cast<const float *>(vc), static_cast<float *>(out), lse, s, ws_o, ws_ml,
+                                    st);
+        if (e == cudaSuccess && s.splits > 1)
+            e = launch_tree_combine<float>(static_cast<float *>(out), lse, s, ws_o, ws_ml, st);
+    } else {
+        e = launch_tree_simt<bf>(static_cast<const bf *>(q), static_cast<const bf *>(kc), static_cast<const bf *>(vc),
+                                 static_cast<bf *>(out), lse, s, ws_o, ws_ml, st);
+        if (e == cudaSuccess && s.splits > 1)
+            e = launch_tree_combine<bf>(static_cast<bf *>(out), lse, s, ws_o, ws_ml, st);
+    }
+    return launch_status(e);
+}
+
+int check_rope(float rope_theta, float rope_factor, int rope_original_max_pos, float beta_fast, float beta_slow,
+               int interleaved)
+{
+    if (!(rope_theta > 1.f && rope_theta < INFINITY) || !(rope_factor > 0.f && rope_factor < INFINITY))
+        return ATTN_SINK_ERR_INVALID_ARG;
+    if (rope_factor > 1.f && (rope_original_max_pos <= 0 || !(beta_fast > beta_slow) || !(beta_slow > 0.f)))
+        return ATTN_SINK_ERR_INVALID_ARG;
+    if (interleaved != 0 && interleaved != 1) return ATTN_SINK_ERR_INVALID_ARG;
+    return ATTN_SINK_OK;
+}
+
 size_t decode_ws_bytes(const DecodeShape &s)
 {
     if (s.splits <= 1) return 0;
@@ -367,15 +460,12 @@ int attn_sink_qkv_prologue(const void *qkv, const float *bias, const int *positi
         return ATTN_SINK_ERR_INVALID_ARG;
     if (D != 64) return ATTN_SINK_ERR_UNSUPPORTED;
     if (!kv_rows && kv_rows_total < T) return ATTN_SINK_ERR_INVALID_ARG;
-    if (!(rope_theta > 1.f && rope_theta < INFINITY) || !(rope_factor > 0.f && rope_factor < INFINITY))
-        return ATTN_SINK_ERR_INVALID_ARG;
-    if (rope_factor > 1.f && (rope_original_max_pos <= 0 || !(beta_fast > beta_slow) || !(beta_slow > 0.f)))
-        return ATTN_SINK_ERR_INVALID_ARG;
-    if (interleaved != 0 && interleaved != 1) return ATTN_SINK_ERR_INVALID_ARG;
+    int rc = check_rope(rope_theta, rope_factor, rope_original_max_pos, beta_fast, beta_slow, interleaved);
+    if (rc != ATTN_SINK_OK) return rc;
     if (!aligned16(qkv) || !aligned16(positions) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out) ||
         (bias && !aligned16(bias)) || (kv_rows && !aligned16(kv_rows)))
         return ATTN_SINK_ERR_MISALIGNED;
-    int rc = ensure_device();
+    rc = ensure_device();
     if (rc != ATTN_SINK_OK) return rc;
     const RopeParams r{rope_theta, rope_factor, (double)rope_original_max_pos, beta_fast, beta_slow, interleaved};
     return launch_status(launch_qkv_prologue(qkv, bias, positions, kv_rows, q_out, k_out, v_out, T, Hq, Hkv,
@@ -507,6 +597,141 @@ int attn_sink_decode_paged(const void *q, const void *k_pages, const void *v_pag
         e = launch_decode_combine<__nv_bfloat16>(seqlens, sinks, static_cast<__nv_bfloat16 *>(out), lse, s, ws_o,
                                                  ws_ml, st);
     return launch_status(e);
+}
+
+size_t attn_sink_decode_tree_workspace_size(int B, int total_q, int max_seqlen_q, int Hq, int Hkv, int D, int Lmax,
+                                            int window, int num_splits, int dtype)
+{
+    if (check_tree(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, num_splits, dtype) != ATTN_SINK_OK) return 0;
+    return tree_ws_bytes(
+        tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, 1.f, num_splits, dtype));
+}
+
+int attn_sink_decode_tree(const void *q, const void *k_cache, const void *v_cache, const int *cu_seqlens_q,
+                          const int *parents, const int *seqlens, const float *sinks, void *out, float *lse, int B,
+                          int total_q, int max_seqlen_q, int Lmax, int Hq, int Hkv, int D, int window, float scale,
+                          int num_splits, void *workspace, size_t ws_bytes, int dtype, void *stream)
+{
+    if (!q || !k_cache || !v_cache || !cu_seqlens_q || !parents || !seqlens || !sinks || !out || !lse)
+        return ATTN_SINK_ERR_INVALID_ARG;
+    const int rc = check_tree(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, num_splits, dtype);
+    if (rc != ATTN_SINK_OK) return rc;
+    TreeShape s = tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale, num_splits, dtype);
+    s.cu_q = cu_seqlens_q;
+    s.parents = parents;
+    s.seqlens = seqlens;
+    s.sinks = sinks;
+    return run_tree(q, k_cache, v_cache, out, lse, s, workspace, ws_bytes, dtype, stream);
+}
+
+int attn_sink_decode_tree_paged(const void *q, const void *k_pages, const void *v_pages, const int *page_table,
+                                const int *cu_seqlens_q, const int *parents, const int *seqlens, const float *sinks,
+                                void *out, float *lse, int B, int total_q, int max_seqlen_q, int max_pages_per_seq,
+                                int page_size, int num_pages, int Hq, int Hkv, int D, int window, float scale,
+                                int num_splits, void *workspace, size_t ws_bytes, int dtype, void *stream)
+{
+    if (!q || !k_pages || !v_pages || !page_table || !cu_seqlens_q || !parents || !seqlens || !sinks || !out || !lse)
+        return ATTN_SINK_ERR_INVALID_ARG;
+    if (!paged_sizes_ok(page_size, max_pages_per_seq, num_pages)) return ATTN_SINK_ERR_INVALID_ARG;
+    const int Lmax = max_pages_per_seq * page_size;
+    const int rc = check_tree(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, num_splits, dtype);
+    if (rc != ATTN_SINK_OK) return rc;
+    TreeShape s = tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale, num_splits, dtype);
+    s.page_size = page_size;
+    s.max_pages = max_pages_per_seq;
+    s.num_pages = num_pages;
+    s.page_table = page_table;
+    s.cu_q = cu_seqlens_q;
+    s.parents = parents;
+    s.seqlens = seqlens;
+    s.sinks = sinks;
+    return run_tree(q, k_pages, v_pages, out, lse, s, workspace, ws_bytes, dtype, stream);
+}
+
+int attn_sink_page_map(const int *cached_lens, const int *new_lens, const int *parents, const int *free_pages,
+                       int *page_table, int *seqlens, int *cu_seqlens, int *positions, int *kv_rows, int *stats, int B,
+                       int total_tokens, int max_pages_per_seq, int page_size, int num_pages, int n_free, void *stream)
+{
+    if (!cached_lens || !new_lens || !page_table || !seqlens || !cu_seqlens || !positions || !kv_rows || !stats)
+        return ATTN_SINK_ERR_INVALID_ARG;
+    if (B <= 0 || total_tokens <= 0 || n_free < 0 || (n_free > 0 && !free_pages)) return ATTN_SINK_ERR_INVALID_ARG;
+    if (!paged_sizes_ok(page_size, max_pages_per_seq, num_pages) ||
+        (long long)num_pages * page_size > 0x7fffffffLL || (long long)B * max_pages_per_seq > 0x7fffffffLL)
+        return ATTN_SINK_ERR_INVALID_ARG;
+    const int *in[] = {cached_lens, new_lens, parents, free_pages};
+    int *outs[] = {page_table, seqlens, cu_seqlens, positions, kv_rows, stats};
+    for (const int *a : in) {
+        if (!aligned16(a)) return ATTN_SINK_ERR_MISALIGNED;
+        for (const int *o : outs)
+            if (a == o) return ATTN_SINK_ERR_INVALID_ARG;
+    }
+    for (const int *o : outs)
+        if (!aligned16(o)) return ATTN_SINK_ERR_MISALIGNED;
+    const int rc = ensure_device();
+    if (rc != ATTN_SINK_OK) return rc;
+    const PageMapShape s{B, total_tokens, max_pages_per_seq, page_size, num_pages, n_free};
+    return launch_status(launch_page_map(cached_lens, new_lens, parents, free_pages, page_table, seqlens, cu_seqlens,
+                                         positions, kv_rows, stats, s, static_cast<cudaStream_t>(stream)));
+}
+
+int attn_sink_qk_norm_prologue(const void *qkv, const float *bias, const float *q_weight, const float *k_weight,
+                               const int *positions, const int *kv_rows, void *q_out, void *k_out, void *v_out, int T,
+                               int Hq, int Hkv, int D, int kv_rows_total, float eps, float rope_theta,
+                               float rope_factor, int rope_original_max_pos, float beta_fast, float beta_slow,
+                               int interleaved, void *stream)
+{
+    if (!qkv || !q_weight || !k_weight || !positions || !q_out || !k_out || !v_out) return ATTN_SINK_ERR_INVALID_ARG;
+    if (T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || kv_rows_total <= 0 || Hq % Hkv != 0)
+        return ATTN_SINK_ERR_INVALID_ARG;
+    if (D != 64 || Hq > 65535) return ATTN_SINK_ERR_UNSUPPORTED;
+    if (!kv_rows && kv_rows_total < T) return ATTN_SINK_ERR_INVALID_ARG;
+    if (!(eps >= 0.f && eps < INFINITY)) return ATTN_SINK_ERR_INVALID_ARG;
+    int rc = check_rope(rope_theta, rope_factor, rope_original_max_pos, beta_fast, beta_slow, interleaved);
+    if (rc != ATTN_SINK_OK) return rc;
+    const void *ptrs[] = {qkv, bias, q_weight, k_weight, positions, kv_rows, q_out, k_out, v_out};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return ATTN_SINK_ERR_MISALIGNED;
+    rc = ensure_device();
+    if (rc != ATTN_SINK_OK) return rc;
+    const RopeParams r{rope_theta, rope_factor, (double)rope_original_max_pos, beta_fast, beta_slow, interleaved};
+    return launch_status(launch_qk_norm_prologue(qkv, bias, QkNorm{q_weight, k_weight, eps}, positions, kv_rows, q_out,
+                                                 k_out, v_out, T, Hq, Hkv, kv_rows_total, r,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+size_t attn_sink_qk_norm_prologue_bwd_workspace_size(int T, int Hq, int Hkv, int D)
+{
+    if (T <= 0 || Hq <= 0 || Hkv <= 0 || D != 64 || Hq % Hkv != 0 || Hq > 65535) return 0;
+    return qk_norm_bwd_workspace_bytes(T, Hq, Hkv);
+}
+
+int attn_sink_qk_norm_prologue_bwd(const void *qkv, const float *bias, const float *q_weight, const float *k_weight,
+                                   const int *positions, const void *dq, const void *dk, const void *dv, void *dqkv,
+                                   float *dbias, float *dq_weight, float *dk_weight, int T, int Hq, int Hkv, int D,
+                                   float eps, float rope_theta, float rope_factor, int rope_original_max_pos,
+                                   float beta_fast, float beta_slow, int interleaved, void *workspace,
+                                   size_t ws_bytes, void *stream)
+{
+    if (!qkv || !q_weight || !k_weight || !positions || !dq || !dk || !dv || !dqkv || !dq_weight || !dk_weight)
+        return ATTN_SINK_ERR_INVALID_ARG;
+    if (dbias && !bias) return ATTN_SINK_ERR_INVALID_ARG;
+    if (T <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return ATTN_SINK_ERR_INVALID_ARG;
+    if (D != 64 || Hq > 65535) return ATTN_SINK_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f && eps < INFINITY)) return ATTN_SINK_ERR_INVALID_ARG;
+    if (dqkv == qkv || dqkv == dq || dqkv == dk || dqkv == dv) return ATTN_SINK_ERR_INVALID_ARG;
+    int rc = check_rope(rope_theta, rope_factor, rope_original_max_pos, beta_fast, beta_slow, interleaved);
+    if (rc != ATTN_SINK_OK) return rc;
+    const void *ptrs[] = {qkv, bias, q_weight, k_weight, positions, dq, dk, dv, dqkv, dbias, dq_weight, dk_weight};
+    for (const void *p : ptrs)
+        if (!aligned16(p)) return ATTN_SINK_ERR_MISALIGNED;
+    if (!workspace || ws_bytes < qk_norm_bwd_workspace_bytes(T, Hq, Hkv)) return ATTN_SINK_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return ATTN_SINK_ERR_MISALIGNED;
+    rc = ensure_device();
+    if (rc != ATTN_SINK_OK) return rc;
+    const RopeParams r{rope_theta, rope_factor, (double)rope_original_max_pos, beta_fast, beta_slow, interleaved};
+    return launch_status(launch_qk_norm_bwd(qkv, bias, QkNorm{q_weight, k_weight, eps}, positions, dq, dk, dv, dqkv,
+                                            dbias, dq_weight, dk_weight, T, Hq, Hkv, r,
+                                            static_cast<float *>(workspace), static_cast<cudaStream_t>(stream)));
 }
 
 namespace {

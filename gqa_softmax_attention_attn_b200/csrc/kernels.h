@@ -129,11 +129,85 @@ cudaError_t launch_decode_bf16(const void *q, const void *kc, const void *vc, co
                                const float *v_scale = nullptr);
 bool decode_bf16_supported(const DecodeShape &s);
 
+// Decode of a tree of drafted tokens per sequence: sequence b's tokens are rows
+// [cu_q[b], cu_q[b + 1]) of q, their keys the last of its seqlens[b] cached ones.
+constexpr int kTreeMaxTokens = 256;
+constexpr int kTreeMaxSplits = 128;
+constexpr int kTreeTile = 64;  // keys per tile; split ranges start on multiples of it
+struct TreeShape {
+    int B, total_q, max_q, Lmax, Hq, Hkv, D, window;
+    float scale;
+    int splits, chunk;  // at most `splits` chunks of `chunk` keys (a multiple of kTreeTile) per sequence
+    int page_size, max_pages, num_pages;  // page_size 0: contiguous cache
+    const int *page_table, *cu_q, *parents, *seqlens;
+    const float *sinks;
+};
+
+// What the kernels need of sequence b (shared by the split and the combine kernels).
+struct TreeSeq {
+    int row0, T;     // its rows of q
+    int len;         // cached keys, the computed drafted tokens' included
+    int cached;      // keys in front of the drafted tokens' own
+    int lo, lo_al;   // first key any of its rows sees; rounded down to a tile
+    int nsplit;      // chunks in use (at least one, which may be empty)
+};
+__device__ __forceinline__ TreeSeq tree_seq(const TreeShape &s, int b)
+{
+    TreeSeq q;
+    const SeqRows r = seq_rows(s.cu_q, b, 0, s.total_q);
+    q.row0 = r.row0;
+    q.T = r.len;
+    q.len = min(max(s.seqlens[b], 0), s.Lmax);
+    q.cached = max(q.len - q.T, 0);
+    q.len = min(q.len, q.cached + s.max_q);  // tokens from max_q on are not computed, nor seen by the others
+    // the shallowest position is the first behind the cached keys
+    q.lo = s.window > 0 ? max(0, q.cached - s.window + 1) : 0;
+    q.lo_al = q.lo / kTreeTile * kTreeTile;
+    q.nsplit = max(1, (q.len - q.lo_al + s.chunk - 1) / s.chunk);
+    return q;
+}
+
+// Exact CUDA-core path, the combine of the splits, and the tensor-core bf16 path.
+template <typename T>
+cudaError_t launch_tree_simt(const T *q, const T *kc, const T *vc, T *out, float *lse, const TreeShape &s, float *ws_o,
+                             float *ws_ml, cudaStream_t st);
+template <typename T>
+cudaError_t launch_tree_combine(T *out, float *lse, const TreeShape &s, const float *ws_o, const float *ws_ml,
+                                cudaStream_t st);
+cudaError_t launch_tree_tc(const void *q, const void *kc, const void *vc, void *out, float *lse, const TreeShape &s,
+                           float *ws_o, float *ws_ml, cudaStream_t st);
+
+// Lengths, offsets, positions, cache rows and new pages of one step's requests.
+struct PageMapShape {
+    int B, total_tokens, max_pages, page_size, num_pages, n_free;
+};
+cudaError_t launch_page_map(const int *cached_lens, const int *new_lens, const int *parents, const int *free_pages,
+                            int *page_table, int *seqlens, int *cu_seqlens, int *positions, int *kv_rows, int *stats,
+                            const PageMapShape &s, cudaStream_t st);
+
 // QKV prologue: bias, YaRN rotary embedding of q and k, split into q / k / v.
 struct RopeParams {
     double base, factor, original_max_pos, beta_fast, beta_slow;
     int interleaved;  // 0: pairs (i, i + D/2); 1: pairs (2i, 2i + 1)
 };
+// rotary frequency of pair i after the YaRN correction, and the factor on cos and sin (host)
+double rope_frequency(const RopeParams &r, int i);
+double rope_attention_factor(const RopeParams &r);
+
+// The prologue with RMS norms of every q and k head in front of the rotation, and its backward.
+struct QkNorm {
+    const float *q_weight, *k_weight;  // [D] fp32
+    float eps;
+};
+cudaError_t launch_qk_norm_prologue(const void *qkv, const float *bias, const QkNorm &n, const int *positions,
+                                    const int *kv_rows, void *q, void *k, void *v, int T, int Hq, int Hkv,
+                                    int kv_rows_total, const RopeParams &r, cudaStream_t st);
+size_t qk_norm_bwd_workspace_bytes(int T, int Hq, int Hkv);
+cudaError_t launch_qk_norm_bwd(const void *qkv, const float *bias, const QkNorm &n, const int *positions,
+                               const void *dq, const void *dk, const void *dv, void *dqkv, float *dbias,
+                               float *dq_weight, float *dk_weight, int T, int Hq, int Hkv, const RopeParams &r,
+                               float *ws, cudaStream_t st);
+
 cudaError_t launch_qkv_prologue(const void *qkv, const float *bias, const int *positions, const int *kv_rows,
                                 void *q, void *k, void *v, int T, int Hq, int Hkv, int kv_rows_total,
                                 const RopeParams &r, cudaStream_t st);

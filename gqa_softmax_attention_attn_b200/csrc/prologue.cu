@@ -52,19 +52,6 @@ struct ProParams {
     double freq[kPairs];       // rotary frequency of each pair after the YaRN correction
 };
 
-// rotary frequency of pair i after the YaRN correction (host, once per call)
-double yarn_freq(const RopeParams &r, int i)
-{
-    const double f = pow(r.base, -2.0 * i / kD);
-    if (!(r.factor > 1.0)) return f;
-    const double lo = kD * log(r.original_max_pos / (2.0 * M_PI * r.beta_fast)) / (2.0 * log(r.base));
-    const double hi = kD * log(r.original_max_pos / (2.0 * M_PI * r.beta_slow)) / (2.0 * log(r.base));
-    double ramp = hi > lo ? (i - lo) / (hi - lo) : (i >= lo ? 1.0 : 0.0);
-    ramp = ramp < 0.0 ? 0.0 : (ramp > 1.0 ? 1.0 : ramp);
-    const double keep = 1.0 - ramp;
-    return f * keep + (f / r.factor) * (1.0 - keep);
-}
-
 // 8 consecutive fp32 bias values (16-byte aligned)
 __device__ __forceinline__ void bias8(const float *b, float (&x)[8])
 {
@@ -211,6 +198,21 @@ __global__ void __launch_bounds__(kThreads) prologue_kernel(const ProParams p)
 
 }  // namespace
 
+// rotary frequency of pair i after the YaRN correction (once per call)
+double rope_frequency(const RopeParams &r, int i)
+{
+    const double f = pow(r.base, -2.0 * i / kD);
+    if (!(r.factor > 1.0)) return f;
+    const double lo = kD * log(r.original_max_pos / (2.0 * M_PI * r.beta_fast)) / (2.0 * log(r.base));
+    const double hi = kD * log(r.original_max_pos / (2.0 * M_PI * r.beta_slow)) / (2.0 * log(r.base));
+    double ramp = hi > lo ? (i - lo) / (hi - lo) : (i >= lo ? 1.0 : 0.0);
+    ramp = ramp < 0.0 ? 0.0 : (ramp > 1.0 ? 1.0 : ramp);
+    const double keep = 1.0 - ramp;
+    return f * keep + (f / r.factor) * (1.0 - keep);
+}
+
+double rope_attention_factor(const RopeParams &r) { return r.factor > 1.0 ? 0.1 * log(r.factor) + 1.0 : 1.0; }
+
 cudaError_t launch_qkv_prologue(const void *qkv, const float *bias, const int *positions, const int *kv_rows,
                                 void *q, void *k, void *v, int T, int Hq, int Hkv, int kv_rows_total,
                                 const RopeParams &r, cudaStream_t st)
@@ -228,8 +230,8 @@ cudaError_t launch_qkv_prologue(const void *qkv, const float *bias, const int *p
     p.Hkv = Hkv;
     p.interleaved = r.interleaved;
     p.kv_rows_total = kv_rows_total;
-    p.attn_factor = r.factor > 1.0 ? 0.1 * log(r.factor) + 1.0 : 1.0;
-    for (int i = 0; i < kPairs; ++i) p.freq[i] = yarn_freq(r, i);
+    p.attn_factor = rope_attention_factor(r);
+    for (int i = 0; i < kPairs; ++i) p.freq[i] = rope_frequency(r, i);
     prologue_kernel<<<(T + kTok - 1) / kTok, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }

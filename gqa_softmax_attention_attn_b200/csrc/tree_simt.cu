@@ -1,0 +1,251 @@
+// tree_simt.cu -- decode of a tree of drafted tokens per sequence on the CUDA
+// cores (the exact path), and the combine of the splits for both paths.
+//
+// Row (token i, query head h) of sequence b sits at position p = cached +
+// depth(i), sees the cached keys j > p - window and, among the drafted tokens'
+// own keys (the sequence's last), those of its ancestors and itself fewer than
+// `window` levels up; its softmax carries the head's sink:
+//   m = max_j s_j, l = sum_j exp(s_j - m), o = sum_j exp(s_j - m) v_j
+// per split of the keys, in log2 units and without the sink, which joins once
+// in the combine (or here, when a sequence needs one split).
+//
+// CTA = (16 rows of one KV head, split, sequence): keys in tiles of 32, lane =
+// key for the scores and lane = (d, d + 32) for the output, so that K and V
+// are read once for 16 rows.  Every score and sum is fp32, each exponential
+// exp2f.  Bound by FMA issue and shared-memory reads (2.5 shared loads per FMA
+// in the scores).
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "kernels.h"
+#include "sm100_ptx.cuh"
+#include "tree_path.cuh"
+
+namespace attn_sink {
+namespace {
+
+constexpr int kD = 64;
+constexpr int kRows = 16;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+__device__ __forceinline__ float warp_max(float x)
+{
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float warp_sum(float x)
+{
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// element offset of (key j, KV head g) in a cache, or -1 (a page outside the pool: zeros)
+__device__ __forceinline__ long long kv_offset(const TreeShape &s, int b, int j, int g)
+{
+    if (s.page_size == 0) return (((long long)b * s.Lmax + j) * s.Hkv + g) * kD;
+    const int page = s.page_table[(size_t)b * s.max_pages + j / s.page_size];
+    if (page < 0 || page >= s.num_pages) return -1;
+    return (((long long)page * s.page_size + j % s.page_size) * s.Hkv + g) * kD;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(128) tree_simt_kernel(const T *__restrict__ q, const T *__restrict__ kc,
+                                                        const T *__restrict__ vc, T *__restrict__ out,
+                                                        float *__restrict__ lse, float *__restrict__ ws_o,
+                                                        float *__restrict__ ws_ml, const TreeShape s, int row_tiles)
+{
+    grid_dep_launch();  // the combine may start its set-up; it waits for this grid
+    __shared__ float qs[kRows][kD];
+    __shared__ float ks[32][kD + 1];
+    __shared__ float vs[32][kD];
+    __shared__ int16_t par[kTreeMaxTokens], depth[kRows];
+    __shared__ uint32_t path[kRows][kPathWords];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rt = blockIdx.x % row_tiles, rest = blockIdx.x / row_tiles;
+    const int g = rest % s.Hkv, c = rest / s.Hkv % s.splits, b = rest / s.Hkv / s.splits;
+    const int G = s.Hq / s.Hkv;
+    const TreeSeq sq = tree_seq(s, b);
+    const int rows = min(sq.T, s.max_q) * G, r0 = rt * kRows;
+    if (c >= sq.nsplit || r0 >= rows) return;  // uniform over the CTA
+    const int nrow = min(kRows, rows - r0);
+    const int kbeg = max(sq.lo, sq.lo_al + c * s.chunk), kend = min(sq.len, sq.lo_al + (c + 1) * s.chunk);
+
+    const int i0 = r0 / G, ntok = (r0 + nrow - 1) / G - i0 + 1;
+    tree_paths(s, sq, i0, ntok, tid, 128, par, path, depth, [] { __syncthreads(); });
+    for (int e = tid; e < nrow * kD; e += 128) {
+        const int r = r0 + e / kD;
+        qs[e / kD][e % kD] = to_f(q[((size_t)(sq.row0 + r / G) * s.Hq + g * G + r % G) * kD + e % kD]);
+    }
+
+    float m[4], l[4], o0[4], o1[4];
+    int tok[4], vis_lo[4];
+#pragma unroll
+    for (int rr = 0; rr < 4; ++rr) {
+        m[rr] = -INFINITY;
+        l[rr] = o0[rr] = o1[rr] = 0.f;
+        const int r = min(r0 + warp * 4 + rr, rows - 1);
+        tok[rr] = r / G - i0;
+        vis_lo[rr] = s.window > 0 ? sq.cached + depth[tok[rr]] - s.window + 1 : 0;
+    }
+    const float C = s.scale * kLog2e;
+    for (int j0 = kbeg; j0 < kend; j0 += 32) {
+        __syncthreads();
+        for (int e = tid; e < 32 * kD; e += 128) {
+            const int j = j0 + e / kD;
+            const long long at = j < kend ? kv_offset(s, b, j, g) : -1;
+            ks[e / kD][e % kD] = at >= 0 ? to_f(kc[at + e % kD]) : 0.f;
+            vs[e / kD][e % kD] = at >= 0 ? to_f(vc[at + e % kD]) : 0.f;
+        }
+        __syncthreads();
+        const int j = j0 + lane, a = j - sq.cached;
+#pragma unroll
+        for (int rr = 0; rr < 4; ++rr) {
+            const int r = warp * 4 + rr;
+            if (r >= nrow) continue;  // uniform over the warp
+            float sc = 0.f;
+#pragma unroll 16
+            for (int d = 0; d < kD; ++d) sc = fmaf(qs[r][d], ks[lane][d], sc);
+            bool see = j < kend && j >= vis_lo[rr];
+            if (a >= 0) see = j < kend && a < kTreeMaxTokens && ((path[tok[rr]][a >> 5] >> (a & 31)) & 1u);
+            sc = see ? sc * C : -INFINITY;
+            const float mn = fmaxf(m[rr], warp_max(sc));
+            const float sub = mn == -INFINITY ? 0.f : mn;  // no finite score so far
+            const float alpha = m[rr] == -INFINITY ? 0.f : exp2f(m[rr] - sub);
+            const float pj = see ? exp2f(sc - sub) : 0.f;
+            l[rr] = l[rr] * alpha + warp_sum(pj);
+            o0[rr] *= alpha;
+            o1[rr] *= alpha;
+#pragma unroll 8
+            for (int jj = 0; jj < 32; ++jj) {
+                const float w = __shfl_sync(0xffffffffu, pj, jj);
+                if (w != 0.f) {  // uniform; a key the row does not see stays out, whatever its value row holds
+                    o0[rr] = fmaf(w, vs[jj][lane], o0[rr]);
+                    o1[rr] = fmaf(w, vs[jj][lane + 32], o1[rr]);
+                }
+            }
+            m[rr] = mn;
+        }
+    }
+#pragma unroll
+    for (int rr = 0; rr < 4; ++rr) {
+        const int r = r0 + warp * 4 + rr;
+        if (r >= rows) continue;
+        const int h = g * G + r % G;
+        const size_t at = (size_t)(sq.row0 + r / G) * s.Hq + h;
+        if (sq.nsplit == 1) {
+            const float sk = s.sinks[h] * kLog2e, M = fmaxf(m[rr], sk);
+            const float fo = m[rr] == -INFINITY ? 0.f : exp2f(m[rr] - M);
+            const float L = l[rr] * fo + (sk == -INFINITY ? 0.f : exp2f(sk - M));
+            const float inv = L > 0.f ? fo / L : 0.f;
+            out[at * kD + lane] = from_f<T>(o0[rr] * inv);
+            out[at * kD + lane + 32] = from_f<T>(o1[rr] * inv);
+            if (lane == 0) lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+        } else {
+            const size_t slot = at * s.splits + c;
+            ws_o[slot * kD + lane] = o0[rr];
+            ws_o[slot * kD + lane + 32] = o1[rr];
+            if (lane == 0) {
+                ws_ml[slot * 2] = m[rr];
+                ws_ml[slot * 2 + 1] = l[rr];
+            }
+        }
+    }
+}
+
+// One warp per (token, query head): M = max(sink, max_c m_c), L = 2^(sink - M)
+// + sum_c l_c 2^(m_c - M), o = sum_c 2^(m_c - M) o_c / L, the splits in order
+// (so the result does not depend on which finished first).
+template <typename T>
+__global__ void __launch_bounds__(128) tree_combine_kernel(T *__restrict__ out, float *__restrict__ lse,
+                                                           const float *__restrict__ ws_o,
+                                                           const float *__restrict__ ws_ml, const TreeShape s)
+{
+    const TreeSeq sq = tree_seq(s, blockIdx.y);
+    const int lane = threadIdx.x & 31;
+    const int w = blockIdx.x * 4 + (threadIdx.x >> 5);  // (token, head) of the sequence
+    grid_dep_wait();  // the partials of the grid ahead (programmatic dependent launch)
+    if (sq.nsplit <= 1 || w >= min(sq.T, s.max_q) * s.Hq) return;
+    const size_t at = (size_t)sq.row0 * s.Hq + w, slot0 = at * s.splits;
+    const float sk = s.sinks[w % s.Hq] * kLog2e;
+    float mc[kTreeMaxSplits / 32], M = sk;
+#pragma unroll
+    for (int k = 0; k < kTreeMaxSplits / 32; ++k) {
+        const int c = 32 * k + lane;
+        mc[k] = c < sq.nsplit ? ws_ml[(slot0 + c) * 2] : -INFINITY;
+        M = fmaxf(M, mc[k]);
+    }
+    M = warp_max(M);
+    float L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kTreeMaxSplits / 32; ++k) {
+        const int c = 32 * k + lane;
+        mc[k] = mc[k] == -INFINITY ? 0.f : exp2f(mc[k] - M);  // from here on the split's weight
+        if (c < sq.nsplit) L += ws_ml[(slot0 + c) * 2 + 1] * mc[k];
+    }
+    L = warp_sum(L) + (sk == -INFINITY ? 0.f : exp2f(sk - M));
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kTreeMaxSplits / 32; ++k) {
+        const int n = min(32, sq.nsplit - 32 * k);
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) {
+            const float f = __shfl_sync(0xffffffffu, mc[k], c);
+            const float2 o = reinterpret_cast<const float2 *>(ws_o + (slot0 + 32 * k + c) * kD)[lane];
+            acc.x = fmaf(f, o.x, acc.x);
+            acc.y = fmaf(f, o.y, acc.y);
+        }
+    }
+    out[at * kD + 2 * lane] = from_f<T>(acc.x * inv);
+    out[at * kD + 2 * lane + 1] = from_f<T>(acc.y * inv);
+    if (lane == 0) lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_tree_simt(const T *q, const T *kc, const T *vc, T *out, float *lse, const TreeShape &s, float *ws_o,
+                             float *ws_ml, cudaStream_t st)
+{
+    const int row_tiles = (s.max_q * (s.Hq / s.Hkv) + kRows - 1) / kRows;
+    const long long ctas = (long long)row_tiles * s.Hkv * s.splits * s.B;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    tree_simt_kernel<T><<<(unsigned)ctas, 128, 0, st>>>(q, kc, vc, out, lse, ws_o, ws_ml, s, row_tiles);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_tree_combine(T *out, float *lse, const TreeShape &s, const float *ws_o, const float *ws_ml,
+                                cudaStream_t st)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)s.max_q * s.Hq + 3) / 4), (unsigned)s.B);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<T>, out, lse, ws_o, ws_ml, s);
+}
+
+#define ATTN_SINK_INSTANTIATE_TREE(T)                                                                             \
+    template cudaError_t launch_tree_simt<T>(const T *, const T *, const T *, T *, float *, const TreeShape &,    \
+                                             float *, float *, cudaStream_t);                                     \
+    template cudaError_t launch_tree_combine<T>(T *, float *, const TreeShape &, const float *, const float *,    \
+                                                cudaStream_t);
+ATTN_SINK_INSTANTIATE_TREE(float)
+ATTN_SINK_INSTANTIATE_TREE(__nv_bfloat16)
+
+}  // namespace attn_sink

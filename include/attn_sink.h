@@ -332,6 +332,155 @@ ATTN_SINK_API size_t attn_sink_decode_paged_workspace_size(int B, int Hq, int D,
                      int page_size, int window, int num_splits);
 
 /*
+ * Decode of drafted tokens ("speculative decoding", multi-token verification):
+ * every sequence brings several query tokens at once, which form a tree -- a
+ * chain when every token follows the one before it -- and whose own keys and
+ * values are already the last ones of the sequence's cache, in token order.
+ * Sequence b owns rows [cu_seqlens_q[b], cu_seqlens_q[b+1]) of q; with T_b
+ * their number, its cache holds seqlens[b] keys, cached_b = seqlens[b] - T_b of
+ * them in front of the drafted ones.  Token i of the sequence at tree depth d_i
+ * (0 for a root) sits at position cached_b + d_i and sees
+ *     the keys j < cached_b with j > cached_b + d_i - window (every one of
+ *     them when window <= 0), and
+ *     the keys cached_b + a of itself and of its ancestors a, those with
+ *     d_i - d_a < window.
+ * Over them it is the operation of attn_sink_fwd: the head's sink joins the
+ * softmax once, and lse includes it.  A token that sees no key gets out = 0
+ * and lse = sink.
+ *   q, out   [total_q, Hq, D]  (dtype)   lse [total_q, Hq] fp32 (token major)
+ *   k_cache, v_cache [B, Lmax, Hkv, D]  (dtype)
+ *   cu_seqlens_q [B + 1] int32, device: non-decreasing from 0, clamped into
+ *            [0, total_q] on the device; a sequence may have no token.  Rows of
+ *            out and lse behind the last sequence are left as they were.
+ *   parents  [total_q] int32, device: index within its own sequence of the
+ *            token each token follows, smaller than its own; an entry outside
+ *            [0, own index) makes the token a root.
+ *   seqlens  [B] int32, device: cached keys of each sequence, its T_b drafted
+ *            ones included, clamped into [0, Lmax].  Keys from seqlens[b] on,
+ *            and keys that the window hides from every token, may hold
+ *            anything; the value row of a key that some but not all tokens of
+ *            a sequence see must be finite (or, for F32, may hold anything).
+ *   max_seqlen_q  host-side upper bound on every T_b, in 1 ..
+ *            ATTN_SINK_TREE_MAX_TOKENS (UNSUPPORTED above); tokens from it on
+ *            are not computed, and their rows left as they were.
+ *   sinks, window, scale: as attn_sink_fwd (scale positive and finite for
+ *            BF16).  dtype F32 (exact) or BF16 (tensor cores); any Hq % Hkv == 0.
+ *   num_splits  0 = choose automatically, else 1..128 chunks of the visible keys
+ *   workspace  device scratch of attn_sink_decode_tree_workspace_size() bytes
+ *            for the same sizes (may be NULL when that is 0); its contents on
+ *            entry do not matter.  Calls that may run at once need their own.
+ * out must not overlap q.  Results are the same from run to run.  Errors as
+ * attn_sink_decode.  Nothing is allocated; asynchronous on `stream`.
+ */
+#define ATTN_SINK_TREE_MAX_TOKENS 256
+ATTN_SINK_API int attn_sink_decode_tree(const void *q, const void *k_cache, const void *v_cache,
+                     const int *cu_seqlens_q, const int *parents, const int *seqlens,
+                     const float *sinks, void *out, float *lse, int B, int total_q,
+                     int max_seqlen_q, int Lmax, int Hq, int Hkv, int D, int window, float scale,
+                     int num_splits, void *workspace, size_t ws_bytes, int dtype, void *stream);
+
+/*
+ * The same over a paged cache (pools, page_table and page_size as for
+ * attn_sink_decode_paged, dtype F32 or BF16).  The table entry and the contents of
+ * a page that no token of its sequence sees may be anything; an entry outside
+ * [0, num_pages) reads zeros.
+ */
+ATTN_SINK_API int attn_sink_decode_tree_paged(const void *q, const void *k_pages, const void *v_pages,
+                     const int *page_table, const int *cu_seqlens_q, const int *parents,
+                     const int *seqlens, const float *sinks, void *out, float *lse, int B,
+                     int total_q, int max_seqlen_q, int max_pages_per_seq, int page_size,
+                     int num_pages, int Hq, int Hkv, int D, int window, float scale, int num_splits,
+                     void *workspace, size_t ws_bytes, int dtype, void *stream);
+
+/* Bytes of workspace of the two calls above (Lmax = max_pages_per_seq *
+ * page_size for a paged cache; 0 when a single split suffices, or for sizes
+ * that the calls refuse). */
+ATTN_SINK_API size_t attn_sink_decode_tree_workspace_size(int B, int total_q, int max_seqlen_q, int Hq,
+                     int Hkv, int D, int Lmax, int window, int num_splits, int dtype);
+
+/*
+ * What one step over a paged cache needs to know about its requests, built on
+ * the device from their lengths: the lengths and offsets the attention calls
+ * take, a position and a cache row for every new token (attn_sink_qkv_prologue
+ * and attn_sink_qk_norm_prologue take them as `positions` and `kv_rows`), and
+ * the page table's entries for the pages the new tokens need.
+ * Request b holds cached_lens[b] tokens in its first ceil(cached_lens[b] /
+ * page_size) pages and gets new_lens[b] new ones (lengths below 0 count as 0):
+ *   seqlens[b]      = cached_lens[b] + new_lens[b]
+ *   cu_seqlens[b]   = sum of new_lens before b   ([B + 1] entries; clamped to
+ *                     total_tokens)
+ *   page_table[b]   its new entries, in order: the next pages of free_pages
+ *                     (requests in order; -1 once the free pages run out);
+ *                     every other entry keeps its value
+ * and token i of request b, row t = cu_seqlens[b] + i:
+ *   positions[t]    = cached_lens[b] + its depth: i without parents, else the
+ *                     number of its ancestors (parents as for
+ *                     attn_sink_decode_tree; a request of more than
+ *                     ATTN_SINK_TREE_MAX_TOKENS new tokens is a chain)
+ *   kv_rows[t]      = page * page_size + slot of cached position
+ *                     cached_lens[b] + i, or -1 where no page holds it (the
+ *                     prologues then write nothing)
+ * Rows behind the last request's tokens, up to total_tokens, get position 0
+ * and cache row -1, so a step captured for more tokens than it holds is safe.
+ *   cached_lens, new_lens [B] int32   free_pages [n_free] int32 (NULL when
+ *   n_free is 0)   page_table [B, max_pages_per_seq] int32   seqlens [B],
+ *   cu_seqlens [B + 1], positions, kv_rows [total_tokens] int32   parents
+ *   [total_tokens] int32 or NULL
+ *   stats [4] int32: sum of new_lens (more than total_tokens: the rest has no
+ *   row), pages taken, of them missing from free_pages, requests longer than
+ *   max_pages_per_seq pages.
+ * All pointers are device memory; the outputs must not overlap the inputs.  free_pages is read
+ * only: the caller drops its first stats[1] entries.  Errors: INVALID_ARG for
+ * null pointers, non-positive sizes, a page size attn_sink_decode_paged does
+ * not take, max_pages_per_seq * page_size, num_pages * page_size or
+ * B * max_pages_per_seq of 2^31 or more, or an output that is one of the inputs.
+ */
+ATTN_SINK_API int attn_sink_page_map(const int *cached_lens, const int *new_lens, const int *parents,
+                     const int *free_pages, int *page_table, int *seqlens, int *cu_seqlens,
+                     int *positions, int *kv_rows, int *stats, int B, int total_tokens,
+                     int max_pages_per_seq, int page_size, int num_pages, int n_free, void *stream);
+
+/*
+ * attn_sink_qkv_prologue for models that normalise every query and key head
+ * ("QK norm"): after the bias and before the rotation each q and k head's D
+ * values y become y / sqrt(mean(y^2) + eps) times the D weights of q or of k.
+ *   q_weight, k_weight [D] fp32, device        eps >= 0, finite
+ * A head of zeros stays zero when eps > 0 (with eps = 0 it is NaN).  Every
+ * other argument, the layouts and the errors are attn_sink_qkv_prologue's; two
+ * tokens must not share a cache row.
+ */
+ATTN_SINK_API int attn_sink_qk_norm_prologue(const void *qkv, const float *bias, const float *q_weight,
+                  const float *k_weight, const int *positions, const int *kv_rows, void *q_out,
+                  void *k_out, void *v_out, int T, int Hq, int Hkv, int D, int kv_rows_total,
+                  float eps, float rope_theta, float rope_factor, int rope_original_max_pos,
+                  float beta_fast, float beta_slow, int interleaved, void *stream);
+
+/*
+ * Its backward (with k and v in token order, kv_rows = NULL): from the
+ * gradients of its outputs the gradients of its inputs.
+ *   dq [T, Hq, D], dk, dv [T, Hkv, D] bf16: as attn_sink_bwd writes them
+ *   dqkv [T, (Hq + 2 Hkv) * D] bf16 (written)
+ *   dbias [(Hq + 2 Hkv) * D] fp32 (written; NULL to leave it out, required to
+ *   be NULL when bias is NULL)
+ *   dq_weight, dk_weight [D] fp32 (written)
+ *   workspace  attn_sink_qk_norm_prologue_bwd_workspace_size(T, Hq, Hkv, D)
+ *   bytes of device scratch; its contents on entry do not matter.
+ * The sums over tokens are fp32 sums of the gradients before they are rounded
+ * to bf16, in a fixed order: results are the same from run to run.  dqkv may be
+ * none of the inputs.  Errors as the forward, WORKSPACE for a missing or short
+ * workspace.
+ */
+ATTN_SINK_API int attn_sink_qk_norm_prologue_bwd(const void *qkv, const float *bias, const float *q_weight,
+                  const float *k_weight, const int *positions, const void *dq, const void *dk,
+                  const void *dv, void *dqkv, float *dbias, float *dq_weight, float *dk_weight, int T,
+                  int Hq, int Hkv, int D, float eps, float rope_theta, float rope_factor,
+                  int rope_original_max_pos, float beta_fast, float beta_slow, int interleaved,
+                  void *workspace, size_t ws_bytes, void *stream);
+
+/* Bytes of workspace attn_sink_qk_norm_prologue_bwd needs (0 for sizes that it refuses). */
+ATTN_SINK_API size_t attn_sink_qk_norm_prologue_bwd_workspace_size(int T, int Hq, int Hkv, int D);
+
+/*
  * Size of the scratch buffer built into the library for
  * attn_sink_decode_noalloc: 32 MiB of device memory, reserved on every GPU
  * that loads the library and held until the process exits.

@@ -287,3 +287,112 @@ def qkv_prologue(qkv, bias, positions, Hq: int, Hkv: int, D: int, base: float, f
     q = rotate(y[:, :Hq], pos, f, a, interleaved)
     k = rotate(y[:, Hq:Hq + Hkv], pos, f, a, interleaved)
     return q, k, y[:, Hq + Hkv:].copy()
+
+
+def tree_depths(parents):
+    """Depth of every token of one sequence; an entry outside [0, own index) makes a root."""
+    d = []
+    for i, a in enumerate(int(x) for x in parents):
+        d.append(d[a] + 1 if 0 <= a < i else 0)
+    return d
+
+
+def decode_tree(q, k_cache, v_cache, cu_seqlens_q, parents, seqlens, sinks, window: int, scale: float):
+    """Drafted tokens over a contiguous cache [B, Lmax, Hkv, D]: every token is one row of `fwd` over the
+    keys it sees, gathered -- its cached keys inside the window at its depth's position, then its ancestors'
+    and its own.  Returns (out [total_q, Hq, D], lse [total_q, Hq]); rows behind the last sequence are NaN."""
+    q, kc, vc, s = _f64(q), _f64(k_cache), _f64(v_cache), _f64(sinks)
+    cu, par, lens = (np.asarray(x.cpu() if hasattr(x, "cpu") else x).astype(int) for x in
+                     (cu_seqlens_q, parents, seqlens))
+    out, lse = np.full_like(q, np.nan), np.full(q.shape[:2], np.nan)
+    for b in range(len(lens)):
+        T = cu[b + 1] - cu[b]
+        p = par[cu[b]:cu[b + 1]]
+        cached = max(lens[b] - T, 0)
+        depth = tree_depths(p)
+        for i in range(T):
+            path, a = [], i
+            while a >= 0:
+                if (window <= 0 or depth[i] - depth[a] < window) and cached + a < lens[b]:
+                    path.append(cached + a)
+                a = p[a] if 0 <= p[a] < a else -1
+            first = max(0, cached + depth[i] - window + 1) if window > 0 else 0
+            keys = list(range(first, cached)) + path
+            t = cu[b] + i
+            if not keys:
+                out[t], lse[t] = 0.0, s
+                continue
+            o, l = fwd(q[None, t:t + 1], kc[b][keys][None], vc[b][keys][None], s, 0, scale)
+            out[t], lse[t] = o[0, 0], l[0, :, 0]
+    return out, lse
+
+
+def page_map(cached_lens, new_lens, free_pages, page_table, total_tokens, page_size, num_pages, parents=None,
+             max_tree=256):
+    """One step's tables from its requests' lengths, request by request and token by token.  Returns
+    (page_table, seqlens, cu_seqlens, positions, kv_rows, stats)."""
+    table = np.array(page_table, dtype=np.int64)
+    free = [int(x) for x in free_pages]
+    width = table.shape[1]
+    pos, rows = np.zeros(total_tokens, dtype=np.int64), np.full(total_tokens, -1, dtype=np.int64)
+    cu, lens = [0], []
+    t, taken, long_ = 0, 0, 0
+    for b, (c, n) in enumerate(zip((max(int(x), 0) for x in cached_lens), (max(int(x), 0) for x in new_lens))):
+        lens.append(c + n)
+        long_ += c + n > width * page_size
+        for e in range(min(-(-c // page_size), width), min(-(-(c + n) // page_size), width)):
+            table[b, e] = free[taken] if taken < len(free) else -1
+            taken += 1
+        par = None if parents is None or n > max_tree else [int(x) for x in parents[t:t + n]]
+        depth = list(range(n)) if par is None else tree_depths(par + [-1] * (n - len(par)))
+        for i in range(n):
+            if t < total_tokens:
+                pos[t] = c + depth[i]
+                page = table[b, (c + i) // page_size] if (c + i) // page_size < width else -1
+                if 0 <= page < num_pages:
+                    rows[t] = page * page_size + (c + i) % page_size
+            t += 1
+        cu.append(min(t, total_tokens))
+    return table, lens, cu, pos, rows, [t, taken, max(taken - len(free), 0), long_]
+
+
+def qk_norm_prologue(qkv, bias, q_weight, k_weight, positions, Hq: int, Hkv: int, D: int, eps: float, base: float,
+                     factor: float = 1.0, original_max_pos: float = 0.0, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, interleaved: bool = False):
+    """`qkv_prologue` with an RMS norm of every q and k head between the bias and the rotation."""
+    y = _f64(qkv)
+    if bias is not None:
+        y = y + _f64(bias)[None, :]
+    y = y.reshape(y.shape[0], Hq + 2 * Hkv, D)
+    pos = np.asarray(positions.cpu() if hasattr(positions, "cpu") else positions, dtype=np.float64)
+    f, a = yarn_frequencies(D, base, factor, original_max_pos, beta_fast, beta_slow)
+    norm = lambda x, w: x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * _f64(w)
+    q = rotate(norm(y[:, :Hq], q_weight), pos, f, a, interleaved)
+    k = rotate(norm(y[:, Hq:Hq + Hkv], k_weight), pos, f, a, interleaved)
+    return q, k, y[:, Hq + Hkv:].copy()
+
+
+def qk_norm_prologue_bwd(qkv, bias, q_weight, k_weight, positions, dq, dk, dv, eps: float, base: float,
+                         factor: float = 1.0, original_max_pos: float = 0.0, beta_fast: float = 32.0,
+                         beta_slow: float = 1.0, interleaved: bool = False):
+    """Gradients (dqkv, dbias, dq_weight, dk_weight) of `qk_norm_prologue`.  With r = (mean(y^2) + eps)^(-1/2),
+    n = y r and u the output gradient rotated back: dw = sum u n, dy = r (w u - n mean(w u n))."""
+    dq, dk, dv = _f64(dq), _f64(dk), _f64(dv)
+    T, Hq, D = dq.shape
+    Hkv = dk.shape[1]
+    y = _f64(qkv)
+    if bias is not None:
+        y = y + _f64(bias)[None, :]
+    y = y.reshape(T, Hq + 2 * Hkv, D)
+    pos = np.asarray(positions.cpu() if hasattr(positions, "cpu") else positions, dtype=np.float64)
+    f, a = yarn_frequencies(D, base, factor, original_max_pos, beta_fast, beta_slow)
+    out, dws = [], []
+    for x, w, g in ((y[:, :Hq], q_weight, dq), (y[:, Hq:Hq + Hkv], k_weight, dk)):
+        u = rotate(g, -pos, f, a, interleaved)  # the transpose of a rotation times a is the opposite one times a
+        r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+        n = x * r
+        dws.append((u * n).sum((0, 1)))
+        wu = u * _f64(w)
+        out.append(r * (wu - n * (wu * n).mean(-1, keepdims=True)))
+    dqkv = np.concatenate(out + [dv], axis=1).reshape(T, -1)
+    return dqkv, dqkv.sum(0), dws[0], dws[1]
