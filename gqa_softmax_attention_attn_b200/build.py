@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libattn_sink.so")
 SOURCES = ["attn_sink_api.cu", "simt_kernels.cu", "fwd_tc.cu", "fwd_band.cu", "decode_tc.cu", "bwd_tc.cu", "prologue.cu",
-           "host_fwd.cu", "tree_simt.cu", "page_map.cu", "qk_norm.cu"]
+           "host_fwd.cu", "tree_simt.cu", "tree_tc.cu", "page_map.cu", "qk_norm.cu"]
 HEADERS = ["kernels.h", "sm100_ptx.cuh", "tree_path.cuh", "selftest.cu"]
 SELFTEST_LIB = os.path.join(LIB_DIR, "libattn_sink_selftest.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

@@ -239,14 +239,12 @@ int run_tree(const void *q, const void *kc, const void *vc, void *out, float *ls
     using bf = __nv_bfloat16;
     cudaError_t e;
     if (dtype == ATTN_SINK_DTYPE_F32) {
-        e = launch_tree_simt<float>(static_cast<const float *>(q), static_cast<const float *>(kc),
-                                    static_cast<const float *>(vc), static_cast<float *>(out), lse, s, ws_o, ws_ml,
-                                    st);
+        e = launch_tree_simt(static_cast<const float *>(q), static_cast<const float *>(kc),
+                             static_cast<const float *>(vc), static_cast<float *>(out), lse, s, ws_o, ws_ml, st);
         if (e == cudaSuccess && s.splits > 1)
             e = launch_tree_combine<float>(static_cast<float *>(out), lse, s, ws_o, ws_ml, st);
     } else {
-        e = launch_tree_simt<bf>(static_cast<const bf *>(q), static_cast<const bf *>(kc), static_cast<const bf *>(vc),
-                                 static_cast<bf *>(out), lse, s, ws_o, ws_ml, st);
+        e = launch_tree_tc(q, kc, vc, out, lse, s, ws_o, ws_ml, st);
         if (e == cudaSuccess && s.splits > 1)
             e = launch_tree_combine<bf>(static_cast<bf *>(out), lse, s, ws_o, ws_ml, st);
     }

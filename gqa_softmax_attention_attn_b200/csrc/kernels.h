@@ -167,10 +167,9 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeShape &s, int b)
     return q;
 }
 
-// Exact CUDA-core path, the combine of the splits, and the tensor-core bf16 path.
-template <typename T>
-cudaError_t launch_tree_simt(const T *q, const T *kc, const T *vc, T *out, float *lse, const TreeShape &s, float *ws_o,
-                             float *ws_ml, cudaStream_t st);
+// Exact fp32 path, the combine of the splits, and the tensor-core bf16 path.
+cudaError_t launch_tree_simt(const float *q, const float *kc, const float *vc, float *out, float *lse,
+                             const TreeShape &s, float *ws_o, float *ws_ml, cudaStream_t st);
 template <typename T>
 cudaError_t launch_tree_combine(T *out, float *lse, const TreeShape &s, const float *ws_o, const float *ws_ml,
                                 cudaStream_t st);

@@ -29,8 +29,6 @@ constexpr int kRows = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <typename T>
 __device__ __forceinline__ T from_f(float x);
 template <>
@@ -58,9 +56,8 @@ __device__ __forceinline__ long long kv_offset(const TreeShape &s, int b, int j,
     return (((long long)page * s.page_size + j % s.page_size) * s.Hkv + g) * kD;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) tree_simt_kernel(const T *__restrict__ q, const T *__restrict__ kc,
-                                                        const T *__restrict__ vc, T *__restrict__ out,
+__global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict__ q, const float *__restrict__ kc,
+                                                        const float *__restrict__ vc, float *__restrict__ out,
                                                         float *__restrict__ lse, float *__restrict__ ws_o,
                                                         float *__restrict__ ws_ml, const TreeShape s, int row_tiles)
 {
@@ -84,7 +81,7 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const T *__restrict__ q,
     tree_paths(s, sq, i0, ntok, tid, 128, par, path, depth, [] { __syncthreads(); });
     for (int e = tid; e < nrow * kD; e += 128) {
         const int r = r0 + e / kD;
-        qs[e / kD][e % kD] = to_f(q[((size_t)(sq.row0 + r / G) * s.Hq + g * G + r % G) * kD + e % kD]);
+        qs[e / kD][e % kD] = q[((size_t)(sq.row0 + r / G) * s.Hq + g * G + r % G) * kD + e % kD];
     }
 
     float m[4], l[4], o0[4], o1[4];
@@ -103,8 +100,8 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const T *__restrict__ q,
         for (int e = tid; e < 32 * kD; e += 128) {
             const int j = j0 + e / kD;
             const long long at = j < kend ? kv_offset(s, b, j, g) : -1;
-            ks[e / kD][e % kD] = at >= 0 ? to_f(kc[at + e % kD]) : 0.f;
-            vs[e / kD][e % kD] = at >= 0 ? to_f(vc[at + e % kD]) : 0.f;
+            ks[e / kD][e % kD] = at >= 0 ? kc[at + e % kD] : 0.f;
+            vs[e / kD][e % kD] = at >= 0 ? vc[at + e % kD] : 0.f;
         }
         __syncthreads();
         const int j = j0 + lane, a = j - sq.cached;
@@ -147,8 +144,8 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const T *__restrict__ q,
             const float fo = m[rr] == -INFINITY ? 0.f : exp2f(m[rr] - M);
             const float L = l[rr] * fo + (sk == -INFINITY ? 0.f : exp2f(sk - M));
             const float inv = L > 0.f ? fo / L : 0.f;
-            out[at * kD + lane] = from_f<T>(o0[rr] * inv);
-            out[at * kD + lane + 32] = from_f<T>(o1[rr] * inv);
+            out[at * kD + lane] = o0[rr] * inv;
+            out[at * kD + lane + 32] = o1[rr] * inv;
             if (lane == 0) lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
         } else {
             const size_t slot = at * s.splits + c;
@@ -213,14 +210,13 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(T *__restrict__ out, 
 
 }  // namespace
 
-template <typename T>
-cudaError_t launch_tree_simt(const T *q, const T *kc, const T *vc, T *out, float *lse, const TreeShape &s, float *ws_o,
-                             float *ws_ml, cudaStream_t st)
+cudaError_t launch_tree_simt(const float *q, const float *kc, const float *vc, float *out, float *lse,
+                             const TreeShape &s, float *ws_o, float *ws_ml, cudaStream_t st)
 {
     const int row_tiles = (s.max_q * (s.Hq / s.Hkv) + kRows - 1) / kRows;
     const long long ctas = (long long)row_tiles * s.Hkv * s.splits * s.B;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    tree_simt_kernel<T><<<(unsigned)ctas, 128, 0, st>>>(q, kc, vc, out, lse, ws_o, ws_ml, s, row_tiles);
+    tree_simt_kernel<<<(unsigned)ctas, 128, 0, st>>>(q, kc, vc, out, lse, ws_o, ws_ml, s, row_tiles);
     return cudaGetLastError();
 }
 
@@ -240,12 +236,9 @@ cudaError_t launch_tree_combine(T *out, float *lse, const TreeShape &s, const fl
     return cudaLaunchKernelEx(&cfg, tree_combine_kernel<T>, out, lse, ws_o, ws_ml, s);
 }
 
-#define ATTN_SINK_INSTANTIATE_TREE(T)                                                                             \
-    template cudaError_t launch_tree_simt<T>(const T *, const T *, const T *, T *, float *, const TreeShape &,    \
-                                             float *, float *, cudaStream_t);                                     \
-    template cudaError_t launch_tree_combine<T>(T *, float *, const TreeShape &, const float *, const float *,    \
+template cudaError_t launch_tree_combine<float>(float *, float *, const TreeShape &, const float *, const float *,
                                                 cudaStream_t);
-ATTN_SINK_INSTANTIATE_TREE(float)
-ATTN_SINK_INSTANTIATE_TREE(__nv_bfloat16)
+template cudaError_t launch_tree_combine<__nv_bfloat16>(__nv_bfloat16 *, float *, const TreeShape &, const float *,
+                                                        const float *, cudaStream_t);
 
 }  // namespace attn_sink
