@@ -8,7 +8,6 @@ library is missing the first call raises ``AttnSinkLibraryMissing``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import threading
@@ -360,28 +359,51 @@ def attn_sink_bwd(q, k, v, sinks, out, dout, lse, dq, dk, dv, dsinks, window: in
     _check(rc, "attn_sink_bwd")
 
 
-def _shape(t, name: str, shape):
-    if tuple(t.shape) != tuple(shape):
+def _take(t, name: str, dtype, shape, dev: int) -> int:
+    """The data pointer of a contiguous tensor of this dtype and shape on device `dev`."""
+    if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.get_device() != dev or dev < 0
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _refuse(t, name, dtype, shape, dev):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same device as the other tensors, cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-@contextlib.contextmanager
-def _on_device_of(first, *tensors):
-    """The device that every tensor lies on, made current for the call (the library launches on the
-    current device)."""
-    if not isinstance(first, torch.Tensor) or not first.is_cuda:
-        raise ValueError("the tensors must be CUDA tensors")
-    for t in tensors:
-        if isinstance(t, torch.Tensor) and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    with torch.cuda.device(first.device):
-        yield
-
-
-def _workspace(workspace):
+def _take_workspace(workspace, dev: int):
     if workspace is None:
-        return 0, 0
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+        return None, 0
+    nbytes = workspace.numel() * workspace.element_size()
+    return _take(workspace, "workspace", workspace.dtype, workspace.shape, dev), nbytes
+
+
+# the current stream's handle without building a Stream object (3 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(where: str, dev: int, stream, *args):
+    """Calls entry point `where` with device `dev` (the tensors') current: the library launches there."""
+    fn = getattr(load(), where)
+    if torch.cuda.current_device() != dev:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _stream(stream))
+    elif stream is None and _raw_stream is not None:
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        rc = fn(*args, _stream(stream))
+    if rc != 0:
+        raise AttnSinkError(rc, where)
 
 
 def attn_sink_decode_tree_workspace_size(B: int, total_q: int, max_seqlen_q: int, Hq: int, Hkv: int, D: int,
@@ -390,18 +412,15 @@ def attn_sink_decode_tree_workspace_size(B: int, total_q: int, max_seqlen_q: int
                                                            int(num_splits), dtype))
 
 
-def _tree_shapes(q, cu_seqlens_q, parents, seqlens, sinks, out, lse, Hkv):
+def _tree_args(q, caches, cache_shape, extra, B, cu_seqlens_q, parents, seqlens, sinks, out, lse):
+    """The pointers that both tree calls share, in the order of the C entry points."""
     total_q, Hq, D = q.shape
-    B = cu_seqlens_q.shape[0] - 1
-    if Hkv <= 0 or Hq % Hkv != 0:
-        raise ValueError(f"{Hq} query heads over {Hkv} KV heads")
-    _shape(out, "out", (total_q, Hq, D))
-    _shape(lse, "lse", (total_q, Hq))
-    _shape(cu_seqlens_q, "cu_seqlens_q", (B + 1,))
-    _shape(parents, "parents", (total_q,))
-    _shape(seqlens, "seqlens", (B,))
-    _shape(sinks, "sinks", (Hq,))
-    return total_q, Hq, D, B
+    dt, dev, i32, f32 = q.dtype, q.get_device(), torch.int32, torch.float32
+    return (_take(q, "q", dt, (total_q, Hq, D), dev), _take(caches[0], "the key cache", dt, cache_shape, dev),
+            _take(caches[1], "the value cache", dt, cache_shape, dev), *extra,
+            _take(cu_seqlens_q, "cu_seqlens_q", i32, (B + 1,), dev), _take(parents, "parents", i32, (total_q,), dev),
+            _take(seqlens, "seqlens", i32, (B,), dev), _take(sinks, "sinks", f32, (Hq,), dev),
+            _take(out, "out", dt, (total_q, Hq, D), dev), _take(lse, "lse", f32, (total_q, Hq), dev))
 
 
 def attn_sink_decode_tree(q, k_cache, v_cache, cu_seqlens_q, parents, seqlens, sinks, out, lse, max_seqlen_q: int,
@@ -409,19 +428,10 @@ def attn_sink_decode_tree(q, k_cache, v_cache, cu_seqlens_q, parents, seqlens, s
     """Drafted tokens q [total_q,Hq,D] (sequence b's rows from cu_seqlens_q [B+1] int32, parents [total_q]
     int32 the index each token follows, -1 for a root) over caches [B,Lmax,Hkv,D] that already hold their
     keys as the last of seqlens [B] int32 -> writes out [total_q,Hq,D], lse [total_q,Hq]."""
-    Lmax, Hkv, dt = k_cache.shape[1], k_cache.shape[2], q.dtype
-    total_q, Hq, D, B = _tree_shapes(q, cu_seqlens_q, parents, seqlens, sinks, out, lse, Hkv)
-    _shape(k_cache, "k_cache", (B, Lmax, Hkv, D))
-    _shape(v_cache, "v_cache", (B, Lmax, Hkv, D))
-    with _on_device_of(q, k_cache, v_cache, cu_seqlens_q, parents, seqlens, sinks, out, lse, workspace):
-        rc = load().attn_sink_decode_tree(_dev(q, "q"), _dev(k_cache, "k_cache", dt), _dev(v_cache, "v_cache", dt),
-                                          _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32),
-                                          _dev(parents, "parents", torch.int32), _dev(seqlens, "seqlens", torch.int32),
-                                          _dev(sinks, "sinks", torch.float32), _dev(out, "out", dt),
-                                          _dev(lse, "lse", torch.float32), B, total_q, int(max_seqlen_q), Lmax, Hq,
-                                          Hkv, D, int(window), float(scale), int(num_splits), *_workspace(workspace),
-                                          _dtype_code(q), _stream(stream))
-    _check(rc, "attn_sink_decode_tree")
+    (total_q, Hq, D), (B, Lmax, Hkv, _), dev = q.shape, k_cache.shape, q.get_device()
+    args = _tree_args(q, (k_cache, v_cache), (B, Lmax, Hkv, D), (), B, cu_seqlens_q, parents, seqlens, sinks, out, lse)
+    _call("attn_sink_decode_tree", dev, stream, *args, B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale,
+          num_splits, *_take_workspace(workspace, dev), _dtype_code(q))
 
 
 def attn_sink_decode_tree_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, parents, seqlens, sinks, out, lse,
@@ -429,50 +439,32 @@ def attn_sink_decode_tree_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, p
                                 stream=None):
     """attn_sink_decode_tree over page pools k/v [num_pages,page_size,Hkv,D] through page_table [B,max_pages]
     int32 (workspace: attn_sink_decode_tree_workspace_size with Lmax = max_pages * page_size)."""
-    num_pages, page_size, Hkv, dt = k_pages.shape[0], k_pages.shape[1], k_pages.shape[2], q.dtype
-    total_q, Hq, D, B = _tree_shapes(q, cu_seqlens_q, parents, seqlens, sinks, out, lse, Hkv)
-    max_pages = page_table.shape[1]
-    _shape(k_pages, "k_pages", (num_pages, page_size, Hkv, D))
-    _shape(v_pages, "v_pages", (num_pages, page_size, Hkv, D))
-    _shape(page_table, "page_table", (B, max_pages))
-    with _on_device_of(q, k_pages, v_pages, page_table, cu_seqlens_q, parents, seqlens, sinks, out, lse, workspace):
-        rc = load().attn_sink_decode_tree_paged(
-            _dev(q, "q"), _dev(k_pages, "k_pages", dt), _dev(v_pages, "v_pages", dt),
-            _dev(page_table, "page_table", torch.int32), _dev(cu_seqlens_q, "cu_seqlens_q", torch.int32),
-            _dev(parents, "parents", torch.int32), _dev(seqlens, "seqlens", torch.int32),
-            _dev(sinks, "sinks", torch.float32), _dev(out, "out", dt), _dev(lse, "lse", torch.float32), B, total_q,
-            int(max_seqlen_q), max_pages, page_size, num_pages, Hq, Hkv, D, int(window), float(scale),
-            int(num_splits), *_workspace(workspace), _dtype_code(q), _stream(stream))
-    _check(rc, "attn_sink_decode_tree_paged")
+    (total_q, Hq, D), (num_pages, page_size, Hkv, _), dev = q.shape, k_pages.shape, q.get_device()
+    B, max_pages = page_table.shape
+    table = _take(page_table, "page_table", torch.int32, (B, max_pages), dev)
+    args = _tree_args(q, (k_pages, v_pages), (num_pages, page_size, Hkv, D), (table,), B, cu_seqlens_q, parents,
+                      seqlens, sinks, out, lse)
+    _call("attn_sink_decode_tree_paged", dev, stream, *args, B, total_q, max_seqlen_q, max_pages, page_size, num_pages,
+          Hq, Hkv, D, window, scale, num_splits, *_take_workspace(workspace, dev), _dtype_code(q))
 
 
 def attn_sink_page_map(cached_lens, new_lens, free_pages, page_table, seqlens, cu_seqlens, positions, kv_rows, stats,
                        page_size: int, num_pages: int, parents=None, stream=None):
     """From cached_lens, new_lens [B] (all int32): writes seqlens [B], cu_seqlens [B+1], positions and kv_rows
     [total_tokens] (rows behind the last request: 0 and -1), stats [4], and the entries of page_table
-    [B,max_pages] for the pages the new tokens need, taken from the front of free_pages; parents
-    [total_tokens] gives the positions of a tree's tokens by their depth."""
-    B, total, max_pages = cached_lens.shape[0], positions.shape[0], page_table.shape[1]
-    _shape(new_lens, "new_lens", (B,))
-    _shape(page_table, "page_table", (B, max_pages))
-    _shape(seqlens, "seqlens", (B,))
-    _shape(cu_seqlens, "cu_seqlens", (B + 1,))
-    _shape(kv_rows, "kv_rows", (total,))
-    _shape(stats, "stats", (4,))
+    [B,max_pages] for the pages the new tokens need, taken from the front of free_pages [n_free] (or None);
+    parents [total_tokens] gives the positions of a tree's tokens by their depth."""
+    B, max_pages = page_table.shape
+    total, dev, i32 = positions.numel(), cached_lens.get_device(), torch.int32
     n_free = 0 if free_pages is None else free_pages.numel()
-    if parents is not None:
-        _shape(parents, "parents", (total,))
-    i32 = torch.int32
-    with _on_device_of(cached_lens, new_lens, free_pages, page_table, seqlens, cu_seqlens, positions, kv_rows, stats,
-                       parents):
-        rc = load().attn_sink_page_map(_dev(cached_lens, "cached_lens", i32), _dev(new_lens, "new_lens", i32),
-                                       _dev(parents, "parents", i32) if parents is not None else None,
-                                       _dev(free_pages, "free_pages", i32) if n_free else None,
-                                       _dev(page_table, "page_table", i32), _dev(seqlens, "seqlens", i32),
-                                       _dev(cu_seqlens, "cu_seqlens", i32), _dev(positions, "positions", i32),
-                                       _dev(kv_rows, "kv_rows", i32), _dev(stats, "stats", i32), B, total, max_pages,
-                                       int(page_size), int(num_pages), n_free, _stream(stream))
-    _check(rc, "attn_sink_page_map")
+    _call("attn_sink_page_map", dev, stream, _take(cached_lens, "cached_lens", i32, (B,), dev),
+          _take(new_lens, "new_lens", i32, (B,), dev),
+          _take(parents, "parents", i32, (total,), dev) if parents is not None else None,
+          _take(free_pages, "free_pages", i32, (n_free,), dev) if n_free else None,
+          _take(page_table, "page_table", i32, (B, max_pages), dev), _take(seqlens, "seqlens", i32, (B,), dev),
+          _take(cu_seqlens, "cu_seqlens", i32, (B + 1,), dev), _take(positions, "positions", i32, (total,), dev),
+          _take(kv_rows, "kv_rows", i32, (total,), dev), _take(stats, "stats", i32, (4,), dev), B, total, max_pages,
+          page_size, num_pages, n_free)
 
 
 def attn_sink_qk_norm_prologue(qkv, bias, q_weight, k_weight, positions, q_out, k_out, v_out, eps: float,
@@ -481,29 +473,17 @@ def attn_sink_qk_norm_prologue(qkv, bias, q_weight, k_weight, positions, q_out, 
                                kv_rows=None, stream=None):
     """attn_sink_qkv_prologue with an RMS norm of every q and k head (weights q_weight, k_weight [D] fp32)
     between the bias and the rotation."""
-    T, Hq, D = q_out.shape
-    rows, Hkv = k_out.shape[0], k_out.shape[1]
-    _shape(qkv, "qkv", (T, (Hq + 2 * Hkv) * D))
-    _shape(k_out, "k_out", (rows, Hkv, D))
-    _shape(v_out, "v_out", (rows, Hkv, D))
-    _shape(positions, "positions", (T,))
-    _shape(q_weight, "q_weight", (D,))
-    _shape(k_weight, "k_weight", (D,))
-    if bias is not None:
-        _shape(bias, "bias", ((Hq + 2 * Hkv) * D,))
-    if kv_rows is not None:
-        _shape(kv_rows, "kv_rows", (T,))
-    bf, f32 = torch.bfloat16, torch.float32
-    with _on_device_of(qkv, bias, q_weight, k_weight, positions, q_out, k_out, v_out, kv_rows):
-        rc = load().attn_sink_qk_norm_prologue(
-            _dev(qkv, "qkv", bf), _dev(bias, "bias", f32) if bias is not None else None,
-            _dev(q_weight, "q_weight", f32), _dev(k_weight, "k_weight", f32),
-            _dev(positions, "positions", torch.int32),
-            _dev(kv_rows, "kv_rows", torch.int32) if kv_rows is not None else None, _dev(q_out, "q_out", bf),
-            _dev(k_out, "k_out", bf), _dev(v_out, "v_out", bf), T, Hq, Hkv, D, rows, float(eps), float(rope_theta),
-            float(rope_factor), int(rope_original_max_pos), float(beta_fast), float(beta_slow),
-            int(bool(interleaved)), _stream(stream))
-    _check(rc, "attn_sink_qk_norm_prologue")
+    (T, Hq, D), (rows, Hkv, _) = q_out.shape, k_out.shape
+    W, dev = (Hq + 2 * Hkv) * D, qkv.get_device()
+    bf, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    _call("attn_sink_qk_norm_prologue", dev, stream, _take(qkv, "qkv", bf, (T, W), dev),
+          _take(bias, "bias", f32, (W,), dev) if bias is not None else None,
+          _take(q_weight, "q_weight", f32, (D,), dev), _take(k_weight, "k_weight", f32, (D,), dev),
+          _take(positions, "positions", i32, (T,), dev),
+          _take(kv_rows, "kv_rows", i32, (T,), dev) if kv_rows is not None else None,
+          _take(q_out, "q_out", bf, (T, Hq, D), dev), _take(k_out, "k_out", bf, (rows, Hkv, D), dev),
+          _take(v_out, "v_out", bf, (rows, Hkv, D), dev), T, Hq, Hkv, D, rows, eps, rope_theta, rope_factor,
+          rope_original_max_pos, beta_fast, beta_slow, int(bool(interleaved)))
 
 
 def attn_sink_qk_norm_prologue_bwd_workspace_size(T: int, Hq: int, Hkv: int, D: int) -> int:
@@ -517,32 +497,18 @@ def attn_sink_qk_norm_prologue_bwd(qkv, bias, q_weight, k_weight, positions, dq,
     """Backward of attn_sink_qk_norm_prologue (k and v in token order): from dq [T,Hq,D], dk, dv [T,Hkv,D] bf16
     writes dqkv [T,(Hq+2Hkv)*D] bf16 and, fp32, dbias [(Hq+2Hkv)*D] (None: left out), dq_weight,
     dk_weight [D]; workspace: attn_sink_qk_norm_prologue_bwd_workspace_size bytes."""
-    T, Hq, D = dq.shape
-    Hkv = dk.shape[1]
-    W = (Hq + 2 * Hkv) * D
-    _shape(qkv, "qkv", (T, W))
-    _shape(dqkv, "dqkv", (T, W))
-    _shape(dk, "dk", (T, Hkv, D))
-    _shape(dv, "dv", (T, Hkv, D))
-    _shape(positions, "positions", (T,))
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight), ("dq_weight", dq_weight),
-                    ("dk_weight", dk_weight)):
-        _shape(t, name, (D,))
-    for name, t in (("bias", bias), ("dbias", dbias)):
-        if t is not None:
-            _shape(t, name, (W,))
+    (T, Hq, D), Hkv = dq.shape, dk.shape[1]
+    W, dev = (Hq + 2 * Hkv) * D, qkv.get_device()
     bf, f32 = torch.bfloat16, torch.float32
-    with _on_device_of(qkv, bias, q_weight, k_weight, positions, dq, dk, dv, dqkv, dbias, dq_weight, dk_weight,
-                       workspace):
-        rc = load().attn_sink_qk_norm_prologue_bwd(
-            _dev(qkv, "qkv", bf), _dev(bias, "bias", f32) if bias is not None else None,
-            _dev(q_weight, "q_weight", f32), _dev(k_weight, "k_weight", f32),
-            _dev(positions, "positions", torch.int32), _dev(dq, "dq", bf), _dev(dk, "dk", bf), _dev(dv, "dv", bf),
-            _dev(dqkv, "dqkv", bf), _dev(dbias, "dbias", f32) if dbias is not None else None,
-            _dev(dq_weight, "dq_weight", f32), _dev(dk_weight, "dk_weight", f32), T, Hq, Hkv, D, float(eps),
-            float(rope_theta), float(rope_factor), int(rope_original_max_pos), float(beta_fast), float(beta_slow),
-            int(bool(interleaved)), *_workspace(workspace), _stream(stream))
-    _check(rc, "attn_sink_qk_norm_prologue_bwd")
+    _call("attn_sink_qk_norm_prologue_bwd", dev, stream, _take(qkv, "qkv", bf, (T, W), dev),
+          _take(bias, "bias", f32, (W,), dev) if bias is not None else None,
+          _take(q_weight, "q_weight", f32, (D,), dev), _take(k_weight, "k_weight", f32, (D,), dev),
+          _take(positions, "positions", torch.int32, (T,), dev), _take(dq, "dq", bf, (T, Hq, D), dev),
+          _take(dk, "dk", bf, (T, Hkv, D), dev), _take(dv, "dv", bf, (T, Hkv, D), dev),
+          _take(dqkv, "dqkv", bf, (T, W), dev), _take(dbias, "dbias", f32, (W,), dev) if dbias is not None else None,
+          _take(dq_weight, "dq_weight", f32, (D,), dev), _take(dk_weight, "dk_weight", f32, (D,), dev), T, Hq, Hkv, D,
+          eps, rope_theta, rope_factor, rope_original_max_pos, beta_fast, beta_slow, int(bool(interleaved)),
+          *_take_workspace(workspace, dev))
 
 
 def attn_sink_get_device_status(stream=None) -> int:
