@@ -186,8 +186,8 @@ TreeShape tree_shape(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, i
     s.D = D;
     s.window = window;
     s.scale = scale;
-    const int tile = dtype == ATTN_SINK_DTYPE_F32 ? 16 : 128;
     const long long all_rows = (long long)max_q * (Hq / Hkv);
+    const int tile = dtype == ATTN_SINK_DTYPE_F32 ? 16 : 128;
     const long long ctas = (long long)B * Hkv * ((all_rows + tile - 1) / tile);
     // keys from the first one a root sees, rounded down to a tile, to the last drafted one
     const long long lw = window > 0 ? (long long)window - 1 + max_q + kTreeTile - 1 : (long long)Lmax;
@@ -212,7 +212,8 @@ int check_tree(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, int D, 
     const int rc = check_common(B, total_q, Lmax, Hq, Hkv, D, dtype);
     if (rc != ATTN_SINK_OK) return rc;
     if (max_q <= 0 || num_splits < 0 || num_splits > kTreeMaxSplits) return ATTN_SINK_ERR_INVALID_ARG;
-    return max_q > kTreeMaxTokens ? ATTN_SINK_ERR_UNSUPPORTED : ATTN_SINK_OK;
+    // positions up to Lmax and a tile or two past them are formed in 32 bits
+    return max_q > kTreeMaxTokens || Lmax > (1 << 30) ? ATTN_SINK_ERR_UNSUPPORTED : ATTN_SINK_OK;
 }
 
 size_t tree_ws_bytes(const TreeShape &s)

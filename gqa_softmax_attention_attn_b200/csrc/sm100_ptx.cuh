@@ -264,6 +264,17 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const CUtensorMap *m
         : "memory");
 }
 
+// the same with the shared-memory addresses already formed
+__device__ __forceinline__ void tma_load_4d_at(uint32_t smem_dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                               int c3, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        : "memory");
+}
+
 // Programmatic dependent launch: a grid launched with the programmatic
 // stream-serialisation attribute may start before the grid ahead of it on the
 // stream has finished; grid_dep_wait() blocks until that grid has completed

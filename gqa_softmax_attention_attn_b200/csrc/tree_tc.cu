@@ -14,7 +14,8 @@
 // HBM, beyond that by the softmax (one exponential per 256 flop).
 //  * CTA = (row tile, KV head, split, sequence); row tiles of one chunk and the
 //    KV heads of one token range are neighbours in the grid, so their K/V rows
-//    meet in L2.  Two CTAs per SM (256 TMEM columns each).
+//    meet in L2.  Two CTAs per SM (256 TMEM columns each): one's start, end and
+//    waits hide behind the other's exponentials.
 //  * A row tile is 128 / C rows, held C times in the 128 lanes of the MMA tile
 //    (C = 4, 2, 1 for up to 32, 64, more rows): copy k's threads take the
 //    k-th part of every tile's keys and write zeros of P elsewhere, once, so
@@ -22,10 +23,18 @@
 //    the exponentials in its dependent chain; the copies' sums join through
 //    shared memory at the end.  The tensor pipe does C times the work, of
 //    which it has plenty to spare while HBM is the limit.
-//  * Warp 0 streams K and V in tiles of 64 keys (128-byte-swizzled TMA boxes, one
-//    a page for small pages, issued by as many lanes) through a ring of kNS
-//    stages; warp 1 issues S = Q K^T into a double-buffered TMEM tile and O += P V
-//    with P from TMEM; warps 2-5, one row (copy) a thread, do the softmax.
+//  * Warps 0-3, one row (copy) a thread, do the softmax; warps 4 and 5 stream K and
+//    V in tiles of 64 keys (128-byte-swizzled TMA boxes, one a page for small
+//    pages) through rings of kNS stages; warp 6 issues S = Q K^T and O += P V, both S and P
+//    double-buffered in tensor memory, so that neither product is in the
+//    softmax warps' chain: S(t + 2) follows P V(t).  One warp issues both, in order, so S(t + 2) being
+//    complete means P V(t) is, and its P buffer free, without another wait.
+//    (Four chains an SM with single buffers, P written over S, hid less: from P
+//    to the next S 1000 to 1700 cycles a tile were in each chain, 1060 cycles a
+//    tile and SM in all.)
+//  * The reference maximum moves in whole powers of two, and only when a tile's
+//    exponentials sum past kSumLimit: scaling what is already summed or
+//    multiplied by it is then exact.
 //  * Masks: a thread's visible keys of a tile are one 64-bit word -- the cached
 //    prefix as a range, the drafted keys as the row's ancestor bits shifted
 //    into place -- and only tiles some row does not see in full apply it.
@@ -47,31 +56,33 @@ namespace {
 constexpr int kM = 128;
 constexpr int kD = 64;
 constexpr int kBN = kTreeTile;
-constexpr int kNS = 5;  // K/V ring stages
-constexpr int kThreads = 192;
+constexpr int kNS = 5;         // K/V ring stages
+constexpr int kThreads = 224;  // warps: 4 softmax, K loads, V loads, MMA issue
+constexpr int kCtasPerSm = 2;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// a tile whose exponentials sum past this moves the row's reference maximum
+// exponentials that sum past this move the row's reference maximum
 constexpr float kSumLimit = 1024.f;
 
 constexpr int kTileBytes = kBN * kD * 2;
+constexpr int kRedStride = 67;  // floats a row (copy) of the exchange at the end
 constexpr int kOffQ = 0;
 constexpr int kOffK = kM * kD * 2;
 constexpr int kOffV = kOffK + kNS * kTileBytes;
-constexpr int kOffPath = kOffV + kNS * kTileBytes;                 // [128][kPathWords] ancestor bits
-constexpr int kOffDepth = kOffPath + kM * kPathWords * 4;          // [128] depths
-constexpr int kOffPar = kOffDepth + kM * 2;                        // [256] parents
+constexpr int kOffPath = kOffV + kNS * kTileBytes;         // [128][kPathWords] ancestor bits
+constexpr int kOffDepth = kOffPath + kM * kPathWords * 4;  // [128] depths
+constexpr int kOffPar = kOffDepth + kM * 2;                // [256] parents
 constexpr int kOffBar = kOffPar + kTreeMaxTokens * 2;
-// q_full, k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_done, drain
-constexpr int kNumBar = 1 + 4 * kNS + 4 + 2;
-constexpr int kOffMisc = kOffBar + kNumBar * 8;                    // TMEM address, abort flag
+// k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_done, o_last
+constexpr int kNumBar = 4 * kNS + 6;
+constexpr int kOffMisc = kOffBar + kNumBar * 8;  // TMEM address, abort flag
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
-constexpr int kRedStride = 67;                                     // floats a row of the copies' exchange
-static_assert(kM * kRedStride * 4 <= 2 * kNS * kTileBytes, "the exchange reuses the K/V ring");
+static_assert(kM * kRedStride * 4 <= kOffPath, "the exchange reuses Q and the K/V ring");
 static_assert(kOffBar % 8 == 0, "barriers on 8 bytes");
-// tensor memory: S and P double-buffered, O
+static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
+// tensor memory: S and P (bf16) double-buffered, O
 constexpr int kTmS = 0, kTmP = 2 * kBN, kTmO = kTmP + kBN, kTmCols = 256;
-static_assert(kTmO + kD <= kTmCols, "tensor memory");
+static_assert(kTmO + kD <= kTmCols && kCtasPerSm * kTmCols <= 512, "tensor memory");
 
 struct TreeTcParams {
     TreeShape s;
@@ -110,7 +121,7 @@ __device__ __forceinline__ uint64_t path_bits(const uint32_t *path, int at)
 }
 
 template <int C>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     tree_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                    const TreeTcParams p)
 {
@@ -119,9 +130,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int kC = kBN / C;    // keys of a tile per thread
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + kOffBar);
-    uint64_t *k_full = q_full + 1, *k_empty = k_full + kNS, *v_full = k_empty + kNS, *v_empty = v_full + kNS;
-    uint64_t *s_full = v_empty + kNS, *p_full = s_full + 2, *o_done = p_full + 2, *drain = o_done + 1;
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + kOffBar);
+    uint64_t *k_empty = k_full + kNS, *v_full = k_empty + kNS, *v_empty = v_full + kNS;
+    uint64_t *s_full = v_empty + kNS, *p_full = s_full + 2, *o_done = p_full + 2, *o_last = o_done + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
 
@@ -140,24 +151,121 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int kend = min((long long)sq.len, (long long)kbeg + p.s.chunk);
     const int n_tiles = kend > kbeg ? (kend - kbeg + kBN - 1) / kBN : 0;
 
-    if (threadIdx.x == 0) {
-        mbar_init(q_full, 128);
-        for (int i = 0; i < kNS; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
+    // the first try and its vote keep the warp converged when the phase is over, or ends while the try is
+    // suspended; only a try that runs out takes the bounded polling loop
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        return __all_sync(0xffffffffu, mbar_wait_slow(bar, parity, abort_flag, p.status, p.timeout_ns));
+    };
+
+    // ---- producers' state.  A tile's slot in its page is 0 for pages of at most a tile, else it advances with
+    // the tiles; `page` holds the pages of 32 boxes, one a lane, and next_page the 32 after them, loaded a
+    // batch ahead.
+    const int ps = p.s.page_size, nb = kBN / p.box_rows, per = 32 / nb;  // boxes of a tile, tiles of a batch
+    int pt = 0, pst = 0, in_batch = 0, page = 0, next_page = 0;
+    uint32_t pph = 1;
+    int slot = kbeg;
+    auto pages = [&](int t0) -> int {
+        // boxes behind the sequence (masked) reuse its last page, so the table is only read within the
+        // sequence's own entries
+        const int lp = (kbeg + t0 * kBN + lane * p.box_rows) / ps;
+        return p.s.page_table[(size_t)b * p.s.max_pages + min(lp, (sq.len - 1) / ps)];
+    };
+    auto start_pages = [&]() {
+        if (ps == 0 || n_tiles == 0) return;
+        slot = kbeg % ps;
+        page = pages(0);
+        if (per < n_tiles) next_page = pages(per);
+    };
+    // tiles up to t_end into their ring: the whole warp runs the loop, so that every operand is warp-uniform,
+    // and one elected lane issues (from a lane == 0 branch an issue took twice as long)
+    auto produce = [&](const CUtensorMap &map, uint64_t *full, uint64_t *empty, uint32_t ring, int t_end) -> bool {
+        for (; pt < t_end; ++pt) {
+            int outer[kBN / 8];
+            outer[0] = b;
+            if (ps > 0) {
+                if (in_batch == per) {
+                    in_batch = 0;
+                    page = next_page;
+                    if (pt + per < n_tiles) next_page = pages(pt + per);
+                }
+#pragma unroll
+                for (int i = 0; i < kBN / 8; ++i)
+                    if (i < nb) outer[i] = __shfl_sync(0xffffffffu, page, in_batch * nb + i);
+                ++in_batch;
+            }
+            if (!wait_all(&empty[pst], pph)) return false;
+            if (elect_one()) {
+                const uint32_t dst = ring + pst * kTileBytes, bar = smem_u32(&full[pst]);
+                mbar_arrive_expect_tx(&full[pst], kTileBytes);
+                tma_load_4d_at(dst, &map, 0, g, slot, outer[0], bar);
+#pragma unroll
+                for (int i = 1; i < kBN / 8; ++i)
+                    if (i < nb) tma_load_4d_at(dst + i * p.box_rows * kD * 2, &map, 0, g, slot, outer[i], bar);
+            }
+            __syncwarp();
+            if (ps == 0 || ps > kBN) {
+                slot += kBN;
+                if (slot == ps) slot = 0;
+            }
+            if (++pst == kNS) {
+                pst = 0;
+                pph ^= 1u;
+            }
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 128);
+        return true;
+    };
+    // every load issued must land before the CTA may exit
+    auto drain = [&](uint64_t *full) {
+        for (int x = 0; x < kNS && x < pt; ++x)
+            wait_noabort(&full[x], (uint32_t)((pt - 1 - x) / kNS) & 1u, p.status, p.timeout_ns);
+    };
+
+    // ---- start: what needs no other warp, side by side
+    const int lrow = warp * 32 + lane;                // softmax warps: TMEM lane
+    const int r = lrow % kRows, copy = lrow / kRows;  // row of the tile, copy of it
+    const bool valid = warp < 4 && r < nrow;
+    const int row = r0 + (valid ? r : 0);
+    const int i0 = r0 / p.G, tok = row / p.G - i0, h = g * p.G + row % p.G;
+    const size_t at = (size_t)(sq.row0 + row / p.G) * p.s.Hq + h;
+    uint32_t(*path)[kPathWords] = reinterpret_cast<uint32_t(*)[kPathWords]>(smem + kOffPath);
+    int16_t *depth = reinterpret_cast<int16_t *>(smem + kOffDepth);
+    if (warp < 4) {
+        // Q: this thread's row into the 128-byte-swizzled operand tile (rows that do not exist: zeros)
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * kD);
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = valid ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4 *>(smem + kOffQ + lrow * 128 + ((k ^ (lrow & 7)) << 4)) = v[k];
+        fence_proxy_async_smem();
+        if (p.s.window > 0 || kend > sq.cached)
+            tree_paths(p.s, sq, i0, (r0 + nrow - 1) / p.G - i0 + 1, lrow, 128,
+                       reinterpret_cast<int16_t *>(smem + kOffPar), path, depth, [] { named_bar_sync(1, 128); });
+    } else if (warp == 4) {
+        if (lane == 0) {
+            for (int i = 0; i < kNS; ++i) {
+                mbar_init(&k_full[i], 1);
+                mbar_init(&k_empty[i], 1);
+                mbar_init(&v_full[i], 1);
+                mbar_init(&v_empty[i], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&s_full[i], 1);
+                mbar_init(&p_full[i], 4);  // the softmax warps
+            }
+            mbar_init(o_done, 1);
+            mbar_init(o_last, 1);
+            *abort_flag = 0;
+            fence_mbar_init();
         }
-        mbar_init(o_done, 1);
-        mbar_init(drain, 1);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 1) {
+        __syncwarp();
+        start_pages();
+        produce(tmK, k_full, k_empty, smem_u32(smem + kOffK), min(n_tiles, kNS));  // (the ring is empty)
+    } else if (warp == 5) {
+        start_pages();
+    } else {
         tmem_alloc(tmem_slot, kTmCols);
         tmem_relinquish();
     }
@@ -166,130 +274,101 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ TMA producer (the whole warp)
-        const int nb = kBN / p.box_rows;  // boxes of a tile, one lane each for K and V
-        const int box = lane % nb, is_v = lane / nb;
-        const int batch = 32 / nb;        // tiles whose page entries one load per lane fetches
-        const int ps = p.s.page_size;
-        if (lane == 0) {
-            tma_prefetch_desc(&tmK);
-            tma_prefetch_desc(&tmV);
-        }
-        int page = 0, t = 0;
-        for (; t < n_tiles; ++t) {
-            const int st = t % kNS;
-            const uint32_t ph = (uint32_t)(t / kNS) & 1u;
-            if (ps > 0 && t % batch == 0) {
-                // the next 32 boxes' pages; boxes behind the sequence (masked) reuse its last page, so
-                // the table is only read within the sequence's own entries
-                const int key = min(kbeg + t * kBN + lane * p.box_rows, sq.len - 1);
-                page = p.s.page_table[(size_t)b * p.s.max_pages + key / ps];
-            }
-            const int my_page = __shfl_sync(0xffffffffu, page, (t % batch) * nb + box);
-            if (!__all_sync(0xffffffffu, mbar_wait(&k_empty[st], ph ^ 1u, abort_flag, p.status, p.timeout_ns) &&
-                                             mbar_wait(&v_empty[st], ph ^ 1u, abort_flag, p.status, p.timeout_ns)))
-                break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&k_full[st], kTileBytes);
-                mbar_arrive_expect_tx(&v_full[st], kTileBytes);
-            }
-            __syncwarp();
-            if (is_v < 2) {
-                const int key = kbeg + t * kBN + box * p.box_rows;
-                uint8_t *dst = smem + (is_v ? kOffV : kOffK) + st * kTileBytes + box * p.box_rows * kD * 2;
-                tma_load_4d(dst, is_v ? &tmV : &tmK, 0, g, ps > 0 ? key % ps : key, ps > 0 ? my_page : b,
-                            is_v ? &v_full[st] : &k_full[st]);
-            }
-        }
-        // every load issued must land before the CTA may exit
-        for (int st = 0; st < kNS && st < t; ++st) {
-            const uint32_t ph = (uint32_t)((t - 1 - st) / kNS) & 1u;
-            wait_noabort(&k_full[st], ph, p.status, p.timeout_ns);
-            wait_noabort(&v_full[st], ph, p.status, p.timeout_ns);
-        }
-    } else if (warp == 1) {
+    if (warp == 4) {
+        produce(tmK, k_full, k_empty, smem_u32(smem + kOffK), n_tiles);
+        drain(k_full);
+    } else if (warp == 5) {
+        produce(tmV, v_full, v_empty, smem_u32(smem + kOffV), n_tiles);
+        drain(v_full);
+    } else if (warp == 6) {
         // ------------------------------------------------------------ MMA issuer (converged, one lane issues)
-        const uint32_t id_s = idesc_bf16_f32(kM, kBN, 0), id_pv = idesc_bf16_f32(kM, kD, 1);
-        const uint32_t q_addr = smem_u32(smem + kOffQ), k_addr = smem_u32(smem + kOffK);
-        auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, p.status, p.timeout_ns));
+        constexpr uint32_t id_s = idesc_bf16_f32(kM, kBN, 0), id_pv = idesc_bf16_f32(kM, kD, 1);
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
+        const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
+        const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + kOffV), kBN * 128, 1024);
+        int kt = 0, kst = 0;  // next tile of S, its stage and phase
+        uint32_t kph = 0;
+        auto issue_s = [&]() {  // one lane
+            const uint64_t kd = k_desc + (uint64_t)((uint32_t)(kst * kTileBytes) >> 4);
+            const uint32_t ts = tmem + kTmS + (kt & 1) * kBN;
+#pragma unroll
+            for (int kk = 0; kk < kD / 16; ++kk)
+                mma_ss(ts, q_desc + (uint64_t)(kk * 32 >> 4), kd + (uint64_t)(kk * 32 >> 4), id_s, kk > 0 ? 1u : 0u);
+            mma_commit(&s_full[kt & 1]);
+            mma_commit(&k_empty[kst]);
         };
-        // O += P(t) V(t)
-        auto issue_pv = [&](int t) -> bool {
-            const int sb = t & 1, st = t % kNS;
-            if (!wait_all(&p_full[sb], (uint32_t)(t >> 1) & 1u)) return false;
-            if (!wait_all(&v_full[st], (uint32_t)(t / kNS) & 1u)) return false;
-            uint8_t *vt = smem + kOffV + st * kTileBytes;
+        auto next_k = [&]() {
+            ++kt;
+            if (++kst == kNS) {
+                kst = 0;
+                kph ^= 1u;
+            }
+        };
+        bool ok = true;
+        while (ok && kt < min(n_tiles, 2)) {
+            ok = wait_all(&k_full[kst], kph);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) issue_s();
+            __syncwarp();
+            next_k();
+        }
+        int st = 0, t = 0;
+        uint32_t ph = 0;
+        for (; ok && t < n_tiles; ++t) {
+            // before P is there: the waits for this V and the K after the next, V's zeros
+            const bool more = kt < n_tiles;
+            if (!wait_all(&v_full[st], ph) || (more && !wait_all(&k_full[kst], kph))) break;
             const int j0 = kbeg + t * kBN;
             if (j0 < sq.lo || j0 + kBN > sq.len) {
                 // value rows no row sees may hold anything (0 x NaN is NaN): zeros
+                uint4 *vt = reinterpret_cast<uint4 *>(smem + kOffV + st * kTileBytes);
                 for (int e = lane; e < kBN * 8; e += 32) {
                     const int j = j0 + (e >> 3);
-                    if (j < sq.lo || j >= sq.len) reinterpret_cast<uint4 *>(vt)[e] = make_uint4(0u, 0u, 0u, 0u);
+                    if (j < sq.lo || j >= sq.len) vt[e] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
             }
+            if (!wait_all(&p_full[t & 1], (uint32_t)(t >> 1) & 1u)) break;
             tc_fence_after();
             if (elect_one()) {
-                const uint32_t va = smem_u32(vt);
+                const uint64_t vd = v_desc + (uint64_t)((uint32_t)(st * kTileBytes) >> 4);
+                const uint32_t tp = tmem + kTmP + (t & 1) * (kBN / 2);
 #pragma unroll
                 for (int kk = 0; kk < kBN / 16; ++kk)
-                    mma_ts(tmem + kTmO, tmem + kTmP + sb * (kBN / 2) + kk * 8,
-                           smem_desc_sw128(va + kk * 2048, kBN * 128, 1024), id_pv, (t > 0 || kk > 0) ? 1u : 0u);
+                    mma_ts(tmem + kTmO, tp + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), id_pv,
+                           (t > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(o_done);
                 mma_commit(&v_empty[st]);
+                if (more) issue_s();  // P(t) being there, S(t) has been read
+                // last of all: once o_last is over, no arrival on this CTA's barriers is still to come
+                if (t == n_tiles - 1) mma_commit(o_last);
             }
             __syncwarp();
-            return true;
-        };
-        bool ok = n_tiles > 0 && wait_all(q_full, 0);
-        for (int t = 0; t < n_tiles && ok; ++t) {
-            const int st = t % kNS, sb = t & 1;
-            if (!wait_all(&k_full[st], (uint32_t)(t / kNS) & 1u)) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t kb = k_addr + st * kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < kD / 16; ++kk)
-                    mma_ss(tmem + kTmS + sb * kBN, smem_desc_sw128(q_addr + kk * 32, 16, 1024),
-                           smem_desc_sw128(kb + kk * 32, 16, 1024), id_s, kk > 0 ? 1u : 0u);
-                mma_commit(&s_full[sb]);
-                mma_commit(&k_empty[st]);
+            if (more) next_k();
+            if (++st == kNS) {
+                st = 0;
+                ph ^= 1u;
             }
-            __syncwarp();
-            if (t >= 1) ok = issue_pv(t - 1);
-            if (ok && t == n_tiles - 1) ok = issue_pv(t);
         }
-        if (elect_one()) mma_commit(drain);
-        __syncwarp();
-        wait_noabort(drain, 0, p.status, p.timeout_ns);
+        // given up half way: what is in flight must still end before tensor memory is freed (nobody else
+        // waits for o_last then)
+        if (kt > 0 && t < n_tiles) {
+            if (elect_one()) mma_commit(o_last);
+            __syncwarp();
+        }
+        if (kt > 0) wait_noabort(o_last, 0, p.status, p.timeout_ns);
     } else {
         // ------------------------------------------------------------ softmax + epilogue
-        const int tid = threadIdx.x - 64;
-        const int quad = warp & 3;
-        const int lrow = quad * 32 + lane;               // TMEM lane
-        const int r = lrow % kRows, copy = lrow / kRows;  // row of the tile, copy of it
-        const bool valid = r < nrow;
-        const bool active = (quad * 32) % kRows < nrow;  // some row of this warp exists
-        const int row = r0 + (valid ? r : 0);
-        const int i0 = r0 / p.G, tok = row / p.G - i0, h = g * p.G + row % p.G;
-        const size_t at = (size_t)(sq.row0 + row / p.G) * p.s.Hq + h;
-        const uint32_t trow = tmem + ((uint32_t)(quad * 32) << 16);
-
-        // Q: this thread's row into the 128-byte-swizzled operand tile (rows that do not exist: zeros)
-        {
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * kD);
-            uint4 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = valid ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4 *>(smem + kOffQ + lrow * 128 + ((k ^ (lrow & 7)) << 4)) = v[k];
-            fence_proxy_async_smem();
-            mbar_arrive(q_full);
-        }
+        const bool active = (warp * 32) % kRows < nrow;  // some row of this warp exists
+        const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
+        const float sink2 = p.s.sinks[h] * kLog2e;
+        // reference maximum in log2 units, a whole number: next to the sink's until a tile moves it
+        float m = rintf(sink2);
+        float l = 0.f;   // running sum, without the sink
+        int vis_lo = 0;  // first cached key this row sees
+        if (p.s.window > 0) vis_lo = max(0, sq.cached + depth[tok] - p.s.window + 1);
         if (C > 1) {
             // P of the keys of the other copies stays zero
             uint32_t z[16];
@@ -298,28 +377,18 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int k = 0; k < kBN / 16; ++k) tmem_st16(trow + kTmP + 16 * k, z);
         }
-        const float sink2 = p.s.sinks[h] * kLog2e;
-        float m = sink2;  // reference maximum, log2 units: the sink's, until a tile moves it
-        float l = 0.f;    // running sum, without the sink
-        uint32_t(*path)[kPathWords] = reinterpret_cast<uint32_t(*)[kPathWords]>(smem + kOffPath);
-        int16_t *depth = reinterpret_cast<int16_t *>(smem + kOffDepth);
-        int vis_lo = 0;  // first cached key this row sees
-        if (p.s.window > 0 || kend > sq.cached) {
-            tree_paths(p.s, sq, i0, (r0 + nrow - 1) / p.G - i0 + 1, tid, 128,
-                       reinterpret_cast<int16_t *>(smem + kOffPar), path, depth, [] { named_bar_sync(1, 128); });
-            if (p.s.window > 0) vis_lo = max(0, sq.cached + depth[tok] - p.s.window + 1);
-        }
         const float2 C2 = make_float2(p.c_log2, p.c_log2);
         bool ok = true;
         for (int t = 0; t < n_tiles; ++t) {
             const int sb = t & 1;
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(&s_full[sb], (uint32_t)(t >> 1) & 1u, abort_flag, p.status, p.timeout_ns))) {
+            const int j0 = kbeg + t * kBN;
+            // S(t) is complete, and with it P V(t - 2): this P buffer is free
+            if (!wait_all(&s_full[sb], (uint32_t)(t >> 1) & 1u)) {
                 ok = false;
                 break;
             }
-            if (!active) {  // no row here: P's values do not matter, only its barrier
-                mbar_arrive(&p_full[sb]);
+            if (!active) {  // no row here: P's values do not matter, only the barrier
+                if (lane == 0) mbar_arrive(&p_full[sb]);
                 continue;
             }
             tc_fence_after();
@@ -330,21 +399,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             float sv[kC];
 #pragma unroll
             for (int k = 0; k < kC; ++k) sv[k] = __uint_as_float(sr[k / 16][k % 16]);
-            const int j0 = kbeg + t * kBN;
-            const bool edge = j0 < vis_lo || j0 + kBN > sq.cached;
-            if (__any_sync(0xffffffffu, edge)) {
+            if (__any_sync(0xffffffffu, j0 < vis_lo || j0 + kBN > sq.cached)) {
                 uint64_t see = range_bits(vis_lo - j0, sq.cached - j0);
-                if (j0 + kBN > sq.cached)
-                    see |= path_bits(path[tok], j0 - sq.cached) & range_bits(0, sq.len - j0);
+                if (j0 + kBN > sq.cached) see |= path_bits(path[tok], j0 - sq.cached) & range_bits(0, sq.len - j0);
                 see >>= copy * kC;
                 const uint32_t see0 = (uint32_t)see, see1 = (uint32_t)(see >> 32);
 #pragma unroll
                 for (int k = 0; k < kC; ++k)
                     sv[k] = ((k < 32 ? see0 : see1) >> (k & 31)) & 1u ? sv[k] : -INFINITY;
             }
-            // P = exp2(S C - m) against the reference maximum, without looking for the tile's: every
-            // exponential is at most their sum, and a sum within kSumLimit (NaN fails the test) keeps
-            // the reference
+            // P = exp2(S C - m) against the reference, without looking for the tile's maximum: every
+            // exponential is at most their sum, and a sum within kSumLimit (NaN fails the test) keeps the
+            // reference
             float2 acc[2];
             auto exp_pass = [&](float neg_m) {
                 const float2 M2 = make_float2(neg_m, neg_m);
@@ -363,131 +429,150 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             };
             exp_pass(m == -INFINITY ? 0.f : -m);
-            float tsum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-            const bool big = !(tsum <= kSumLimit) || m == -INFINITY;
-            bool rescale = false;
-            float alpha = 1.f;
+            float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            const bool big = !(sum <= kSumLimit) || m == -INFINITY;
             if (__any_sync(0xffffffffu, big)) {
-                float mx[8];
+                float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) mx[k] = -INFINITY;
+                for (int k = 4; k < kC; k += 4)
 #pragma unroll
-                for (int k = 0; k < kC; k += 16)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mx[e] = fmax3(mx[e], sv[k + e], sv[k + 8 + e]);
-                const float tmax = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-                const float m_new = fmaxf(m, tmax * p.c_log2);
-                rescale = big && m_new > m;
-                if (__any_sync(0xffffffffu, rescale)) {
-                    if (rescale) {
-                        alpha = m == -INFINITY ? 0.f : ex2(m - m_new);
-                        m = m_new;
-                    }
+                    for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], sv[k + e]);
+                const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c_log2;
+                const bool move = big && tmax > m;
+                if (__any_sync(0xffffffffu, move)) {
+                    // up by a whole number of powers of two, so that the scaling is exact
+                    const float m_new = move ? (m == -INFINITY ? ceilf(tmax) : m + ceilf(tmax - m)) : m;
+                    const float d = m_new - m;  // 0 where the reference stays, infinite where there was none
+                    const float alpha = d > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)d) << 23);
+                    m = m_new;
+                    l *= alpha;
                     exp_pass(m == -INFINITY ? 0.f : -m);
-                    tsum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                }
-            }
-            l = l * alpha + tsum;
-            if (t > 0) {
-                // O holds the products of the tiles before once P V(t - 1) completes; waited on at every
-                // tile, so that the parity is never more than one phase behind
-                if (!__all_sync(0xffffffffu,
-                                mbar_wait(o_done, (uint32_t)(t - 1) & 1u, abort_flag, p.status, p.timeout_ns))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (__any_sync(0xffffffffu, rescale)) {
+                    sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                    if (t > 0) {
+                        // O must hold the tile before, too.  (P V(t - 2) is complete, P V(t) not issued:
+                        // the parity is unambiguous although other phases go unobserved.)
+                        if (!wait_all(o_done, (uint32_t)(t - 1) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < kD / 16; ++k) {
-                        uint32_t o[16];
-                        tmem_ld16(trow + kTmO + 16 * k, o);
-                        tmem_wait_ld();
+                        for (int k = 0; k < kD / 16; ++k) {
+                            uint32_t o[16];
+                            tmem_ld16(trow + kTmO + 16 * k, o);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st16(trow + kTmO + 16 * k, o);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tmem_st16(trow + kTmO + 16 * k, o);
+                        }
                     }
                 }
             }
+            l += sum;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(&p_full[sb]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[sb]);
         }
-        if (ok && active && n_tiles > 0)
-            ok = __all_sync(0xffffffffu, mbar_wait(o_done, (uint32_t)(n_tiles - 1) & 1u, abort_flag, p.status,
-                                                   p.timeout_ns));
+        const bool any = n_tiles > 0;
+        if (ok && active && any) ok = wait_all(o_last, 0);
         // -------------------------------------------------------- epilogue
-        constexpr int kOut = kD / C;  // output columns of a thread: [copy kOut, + kOut)
-        float o[kD];
-        if (ok && active && n_tiles > 0) {
-            tc_fence_after();
-#pragma unroll
-            for (int k = 0; k < kD / 16; ++k) {
-                uint32_t x[16];
+        tc_fence_after();
+        // 16 columns of O
+        auto load_o = [&](int k, float (&o)[16]) {
+            uint32_t x[16];
+            if (any) {
                 tmem_ld16(trow + kTmO + 16 * k, x);
                 tmem_wait_ld();
+            }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[16 * k + e] = __uint_as_float(x[e]);
+            for (int e = 0; e < 16; ++e) o[e] = any ? __uint_as_float(x[e]) : 0.f;
+        };
+        const size_t part = at * p.s.splits + c;
+        float L = l, scale_o = 1.f;
+        // the row's statistics are final: a partial of its split, or the sink's share and the norm
+        auto finish_row = [&](bool write) {
+            if (sq.nsplit > 1) {
+                if (write) *reinterpret_cast<float2 *>(p.ws_ml + part * 2) = make_float2(m, L);
+                return;
+            }
+            // m starts next to the sink and only grows
+            L += sink2 == -INFINITY ? 0.f : ex2(sink2 - m);
+            scale_o = L > 0.f ? 1.f / L : 0.f;
+            if (write) p.lse[at] = L > 0.f ? (m + log2f(L)) * kLn2 : -INFINITY;
+        };
+        // 8 columns of the row from column d on
+        auto store_o = [&](int d, const float *o) {
+            if (sq.nsplit > 1) {
+                float4 *dst = reinterpret_cast<float4 *>(p.ws_o + part * kD + d);
+                dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+            } else {
+                *reinterpret_cast<uint4 *>(p.out + at * kD + d) =
+                    make_uint4(pack_bf16x2(o[0] * scale_o, o[1] * scale_o), pack_bf16x2(o[2] * scale_o, o[3] * scale_o),
+                               pack_bf16x2(o[4] * scale_o, o[5] * scale_o), pack_bf16x2(o[6] * scale_o, o[7] * scale_o));
+            }
+        };
+        if (C == 1) {
+            if (ok && active) {
+                if (valid) finish_row(true);
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) {
+                    float o[16];
+                    load_o(k, o);
+                    if (valid) {
+                        store_o(16 * k, o);
+                        store_o(16 * k + 8, o + 8);
+                    }
+                }
             }
         } else {
-#pragma unroll
-            for (int k = 0; k < kD; ++k) o[k] = 0.f;
-        }
-        if (C > 1) {
-            // the copies' statistics and sums join, each thread its part of the columns.  Every load
-            // and product of the ring has completed: it is free.
-            // (an expired wait leaves the exchange unused: the barrier below is reached by all 128)
-            float *red = reinterpret_cast<float *>(smem + kOffK);
-            if (active) {
+            // The copies of a row join through Q and the ring, which are free (every product, and so every load
+            // it read, has completed); thread (row, copy) takes the copy-th part of the columns.  The barrier
+            // is reached by all 128 threads, after an expired wait too.
+            constexpr int kOut = kD / C;
+            float *red = reinterpret_cast<float *>(smem);
+            if (!ok) *abort_flag = 1;
+            if (ok && active) {
                 float *me = red + lrow * kRedStride;
 #pragma unroll
-                for (int k = 0; k < kD; ++k) me[k] = o[k];
+                for (int k = 0; k < kD / 16; ++k) {
+                    float o[16];
+                    load_o(k, o);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) me[16 * k + e] = o[e];
+                }
                 me[kD] = m;
                 me[kD + 1] = l;
             }
-            if (!ok) *abort_flag = 1;
             named_bar_sync(1, 128);
-            if (*abort_flag) ok = false;
-            if (ok && active) {
-                float M = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < C; ++k) M = fmaxf(M, red[(k * kRows + r) * kRedStride + kD]);
-                l = 0.f;
-#pragma unroll
-                for (int e = 0; e < kOut; ++e) o[e] = 0.f;
+            if (*abort_flag == 0 && valid) {
+                const float *you = red + r * kRedStride;  // copy k: k * kRows rows on
+                float f[C];
+                m = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < C; ++k) {
-                    const float *you = red + (k * kRows + r) * kRedStride;
-                    const float f = you[kD] == -INFINITY ? 0.f : ex2(you[kD] - M);
-                    l = fmaf(f, you[kD + 1], l);
-#pragma unroll
-                    for (int e = 0; e < kOut; ++e) o[e] = fmaf(f, you[copy * kOut + e], o[e]);
+                    f[k] = you[k * kRows * kRedStride + kD];
+                    m = fmaxf(m, f[k]);
                 }
-                m = M;
-            }
-        }
-        if (ok && valid) {
-            if (sq.nsplit == 1) {
-                // m starts at the sink, so it is the larger of the two
-                const float L = l + (sink2 == -INFINITY ? 0.f : ex2(sink2 - m));
-                const float inv = L > 0.f ? 1.f / L : 0.f;
-                uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * kD + copy * kOut);
+                L = 0.f;
 #pragma unroll
-                for (int k = 0; k < kOut / 8; ++k)
-                    dst[k] = make_uint4(pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                        pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                        pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                        pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-                if (copy == 0) p.lse[at] = L > 0.f ? (m + log2f(L)) * kLn2 : -INFINITY;
-            } else {
-                const size_t slot = at * p.s.splits + c;
-                float4 *dst = reinterpret_cast<float4 *>(p.ws_o + slot * kD + copy * kOut);
+                for (int k = 0; k < C; ++k) {
+                    f[k] = f[k] == -INFINITY ? 0.f : ex2(f[k] - m);
+                    L = fmaf(f[k], you[k * kRows * kRedStride + kD + 1], L);
+                }
+                finish_row(copy == 0);
 #pragma unroll
-                for (int k = 0; k < kOut / 4; ++k)
-                    dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                if (copy == 0) {
-                    p.ws_ml[slot * 2] = m;
-                    p.ws_ml[slot * 2 + 1] = l;
+                for (int x = 0; x < kOut / 8; ++x) {
+                    const int d = copy * kOut + 8 * x;
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < C; ++k)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = fmaf(f[k], you[k * kRows * kRedStride + d + e], o[e]);
+                    store_o(d, o);
                 }
             }
         }
@@ -495,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == 6) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, kTmCols);

@@ -348,7 +348,7 @@ ATTN_SINK_API size_t attn_sink_decode_paged_workspace_size(int B, int Hq, int D,
  * softmax once, and lse includes it.  A token that sees no key gets out = 0
  * and lse = sink.
  *   q, out   [total_q, Hq, D]  (dtype)   lse [total_q, Hq] fp32 (token major)
- *   k_cache, v_cache [B, Lmax, Hkv, D]  (dtype)
+ *   k_cache, v_cache [B, Lmax, Hkv, D]  (dtype); Lmax at most 2^30 (UNSUPPORTED above)
  *   cu_seqlens_q [B + 1] int32, device: non-decreasing from 0, clamped into
  *            [0, total_q] on the device; a sequence may have no token.  Rows of
  *            out and lse behind the last sequence are left as they were.
