@@ -171,10 +171,10 @@ DecodeShape decode_shape_paged(int B, int max_pages, int page_size, int num_page
     return s;
 }
 
-// The work of one CTA of the tree decode spans `rows` rows (a KV head's query
-// heads times the sequence's tokens, at most a row tile) and one chunk of keys.
+// The fp32 path cuts every sequence into equal chunks; a CTA takes 16 rows (a KV head's query heads times the
+// sequence's tokens) of one.
 TreeShape tree_shape(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, int D, int window, float scale,
-                     int num_splits, int dtype)
+                     int num_splits)
 {
     TreeShape s{};
     s.B = B;
@@ -186,19 +186,13 @@ TreeShape tree_shape(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, i
     s.D = D;
     s.window = window;
     s.scale = scale;
-    const long long all_rows = (long long)max_q * (Hq / Hkv);
-    const int tile = dtype == ATTN_SINK_DTYPE_F32 ? 16 : 128;
-    const long long ctas = (long long)B * Hkv * ((all_rows + tile - 1) / tile);
+    const long long rows = (long long)max_q * (Hq / Hkv);
+    const long long ctas = (long long)B * Hkv * ((rows + 15) / 16);
     // keys from the first one a root sees, rounded down to a tile, to the last drafted one
     const long long lw = window > 0 ? (long long)window - 1 + max_q + kTreeTile - 1 : (long long)Lmax;
     const long long lvis = lw < Lmax ? lw : Lmax;
-    long long splits = num_splits;
-    long long least = kTreeTile;
-    if (splits == 0) {
-        splits = (B == 1 ? 1 : 16) * 296 / ctas;
-        const long long rows = all_rows < tile ? all_rows : tile;
-        least = 16 * rows > 256 ? 16 * rows : 256;
-    }
+    long long splits = num_splits > 0 ? num_splits : 16 * 296 / ctas;
+    const long long least = num_splits > 0 ? kTreeTile : 256;
     splits = splits < 1 ? 1 : (splits > kTreeMaxSplits ? kTreeMaxSplits : splits);
     long long chunk = (lvis + splits - 1) / splits;
     chunk = ((chunk > least ? chunk : least) + kTreeTile - 1) / kTreeTile * kTreeTile;
@@ -216,40 +210,33 @@ int check_tree(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, int D, 
     return max_q > kTreeMaxTokens || Lmax > (1 << 30) ? ATTN_SINK_ERR_UNSUPPORTED : ATTN_SINK_OK;
 }
 
-size_t tree_ws_bytes(const TreeShape &s)
+size_t tree_ws_bytes(const TreeShape &s, int num_splits, int dtype)
 {
+    if (dtype == ATTN_SINK_DTYPE_BF16) return tree_tc_workspace_bytes(s, num_splits);
     return s.splits <= 1 ? 0 : (size_t)s.total_q * s.Hq * s.splits * (s.D + 2) * sizeof(float);
 }
 
 // both cache layouts, once the sizes are checked
-int run_tree(const void *q, const void *kc, const void *vc, void *out, float *lse, TreeShape &s, void *workspace,
-             size_t ws_bytes, int dtype, void *stream)
+int run_tree(const void *q, const void *kc, const void *vc, void *out, float *lse, const TreeShape &s, int num_splits,
+             void *workspace, size_t ws_bytes, int dtype, void *stream)
 {
     if (dtype == ATTN_SINK_DTYPE_BF16 && !(s.scale > 0.f && s.scale < INFINITY)) return ATTN_SINK_ERR_UNSUPPORTED;
     const void *ptrs[] = {q, kc, vc, out, lse, s.page_table, s.cu_q, s.parents, s.seqlens, s.sinks};
     for (const void *p : ptrs)
         if (!aligned16(p)) return ATTN_SINK_ERR_MISALIGNED;
-    const size_t need = tree_ws_bytes(s);
+    const size_t need = tree_ws_bytes(s, num_splits, dtype);
     if (need > 0 && (!workspace || ws_bytes < need)) return ATTN_SINK_ERR_WORKSPACE;
     if (need > 0 && !aligned16(workspace)) return ATTN_SINK_ERR_MISALIGNED;
     const int rc = ensure_device();
     if (rc != ATTN_SINK_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == ATTN_SINK_DTYPE_BF16)
+        return launch_status(launch_tree_tc(q, kc, vc, out, lse, s, num_splits, workspace, st));
     float *ws_o = static_cast<float *>(workspace);
     float *ws_ml = need > 0 ? ws_o + (size_t)s.total_q * s.Hq * s.splits * s.D : nullptr;
-    using bf = __nv_bfloat16;
-    cudaError_t e;
-    if (dtype == ATTN_SINK_DTYPE_F32) {
-        e = launch_tree_simt(static_cast<const float *>(q), static_cast<const float *>(kc),
-                             static_cast<const float *>(vc), static_cast<float *>(out), lse, s, ws_o, ws_ml, st);
-        if (e == cudaSuccess && s.splits > 1)
-            e = launch_tree_combine<float>(static_cast<float *>(out), lse, s, ws_o, ws_ml, st);
-    } else {
-        e = launch_tree_tc(q, kc, vc, out, lse, s, ws_o, ws_ml, st);
-        if (e == cudaSuccess && s.splits > 1)
-            e = launch_tree_combine<bf>(static_cast<bf *>(out), lse, s, ws_o, ws_ml, st);
-    }
-    return launch_status(e);
+    return launch_status(launch_tree_simt(static_cast<const float *>(q), static_cast<const float *>(kc),
+                                          static_cast<const float *>(vc), static_cast<float *>(out), lse, s, ws_o,
+                                          ws_ml, st));
 }
 
 int check_rope(float rope_theta, float rope_factor, int rope_original_max_pos, float beta_fast, float beta_slow,
@@ -602,8 +589,8 @@ size_t attn_sink_decode_tree_workspace_size(int B, int total_q, int max_seqlen_q
                                             int window, int num_splits, int dtype)
 {
     if (check_tree(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, num_splits, dtype) != ATTN_SINK_OK) return 0;
-    return tree_ws_bytes(
-        tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, 1.f, num_splits, dtype));
+    return tree_ws_bytes(tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, 1.f, num_splits), num_splits,
+                         dtype);
 }
 
 int attn_sink_decode_tree(const void *q, const void *k_cache, const void *v_cache, const int *cu_seqlens_q,
@@ -615,12 +602,12 @@ int attn_sink_decode_tree(const void *q, const void *k_cache, const void *v_cach
         return ATTN_SINK_ERR_INVALID_ARG;
     const int rc = check_tree(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, num_splits, dtype);
     if (rc != ATTN_SINK_OK) return rc;
-    TreeShape s = tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale, num_splits, dtype);
+    TreeShape s = tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale, num_splits);
     s.cu_q = cu_seqlens_q;
     s.parents = parents;
     s.seqlens = seqlens;
     s.sinks = sinks;
-    return run_tree(q, k_cache, v_cache, out, lse, s, workspace, ws_bytes, dtype, stream);
+    return run_tree(q, k_cache, v_cache, out, lse, s, num_splits, workspace, ws_bytes, dtype, stream);
 }
 
 int attn_sink_decode_tree_paged(const void *q, const void *k_pages, const void *v_pages, const int *page_table,
@@ -635,7 +622,7 @@ int attn_sink_decode_tree_paged(const void *q, const void *k_pages, const void *
     const int Lmax = max_pages_per_seq * page_size;
     const int rc = check_tree(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, num_splits, dtype);
     if (rc != ATTN_SINK_OK) return rc;
-    TreeShape s = tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale, num_splits, dtype);
+    TreeShape s = tree_shape(B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale, num_splits);
     s.page_size = page_size;
     s.max_pages = max_pages_per_seq;
     s.num_pages = num_pages;
@@ -644,7 +631,7 @@ int attn_sink_decode_tree_paged(const void *q, const void *k_pages, const void *
     s.parents = parents;
     s.seqlens = seqlens;
     s.sinks = sinks;
-    return run_tree(q, k_pages, v_pages, out, lse, s, workspace, ws_bytes, dtype, stream);
+    return run_tree(q, k_pages, v_pages, out, lse, s, num_splits, workspace, ws_bytes, dtype, stream);
 }
 
 int attn_sink_page_map(const int *cached_lens, const int *new_lens, const int *parents, const int *free_pages,

@@ -137,7 +137,8 @@ constexpr int kTreeTile = 64;  // keys per tile; split ranges start on multiples
 struct TreeShape {
     int B, total_q, max_q, Lmax, Hq, Hkv, D, window;
     float scale;
-    int splits, chunk;  // at most `splits` chunks of `chunk` keys (a multiple of kTreeTile) per sequence
+    // fp32 path: at most `splits` chunks of `chunk` keys (a multiple of kTreeTile) per sequence
+    int splits, chunk;
     int page_size, max_pages, num_pages;  // page_size 0: contiguous cache
     const int *page_table, *cu_q, *parents, *seqlens;
     const float *sinks;
@@ -149,7 +150,7 @@ struct TreeSeq {
     int len;         // cached keys, the computed drafted tokens' included
     int cached;      // keys in front of the drafted tokens' own
     int lo, lo_al;   // first key any of its rows sees; rounded down to a tile
-    int nsplit;      // chunks in use (at least one, which may be empty)
+    int nsplit;      // chunks in use (at least one, which may be empty); fp32 path
 };
 __device__ __forceinline__ TreeSeq tree_seq(const TreeShape &s, int b)
 {
@@ -167,14 +168,12 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeShape &s, int b)
     return q;
 }
 
-// Exact fp32 path, the combine of the splits, and the tensor-core bf16 path.
+// Exact fp32 path (with the combine of its splits), and the tensor-core bf16 path.
 cudaError_t launch_tree_simt(const float *q, const float *kc, const float *vc, float *out, float *lse,
                              const TreeShape &s, float *ws_o, float *ws_ml, cudaStream_t st);
-template <typename T>
-cudaError_t launch_tree_combine(T *out, float *lse, const TreeShape &s, const float *ws_o, const float *ws_ml,
-                                cudaStream_t st);
+size_t tree_tc_workspace_bytes(const TreeShape &s, int num_splits);
 cudaError_t launch_tree_tc(const void *q, const void *kc, const void *vc, void *out, float *lse, const TreeShape &s,
-                           float *ws_o, float *ws_ml, cudaStream_t st);
+                           int num_splits, void *ws, cudaStream_t st);
 
 // Lengths, offsets, positions, cache rows and new pages of one step's requests.
 struct PageMapShape {

@@ -1,5 +1,5 @@
 // tree_simt.cu -- decode of a tree of drafted tokens per sequence on the CUDA
-// cores (the exact path), and the combine of the splits for both paths.
+// cores (the exact fp32 path), and the combine of its splits.
 //
 // Row (token i, query head h) of sequence b sits at position p = cached +
 // depth(i), sees the cached keys j > p - window and, among the drafted tokens'
@@ -28,13 +28,6 @@ constexpr int kD = 64;
 constexpr int kRows = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ float from_f<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 __device__ __forceinline__ float warp_max(float x)
 {
@@ -162,8 +155,7 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
 // One warp per (token, query head): M = max(sink, max_c m_c), L = 2^(sink - M)
 // + sum_c l_c 2^(m_c - M), o = sum_c 2^(m_c - M) o_c / L, the splits in order
 // (so the result does not depend on which finished first).
-template <typename T>
-__global__ void __launch_bounds__(128) tree_combine_kernel(T *__restrict__ out, float *__restrict__ lse,
+__global__ void __launch_bounds__(128) tree_combine_kernel(float *__restrict__ out, float *__restrict__ lse,
                                                            const float *__restrict__ ws_o,
                                                            const float *__restrict__ ws_ml, const TreeShape s)
 {
@@ -203,8 +195,7 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(T *__restrict__ out, 
             acc.y = fmaf(f, o.y, acc.y);
         }
     }
-    out[at * kD + 2 * lane] = from_f<T>(acc.x * inv);
-    out[at * kD + 2 * lane + 1] = from_f<T>(acc.y * inv);
+    reinterpret_cast<float2 *>(out + at * kD)[lane] = make_float2(acc.x * inv, acc.y * inv);
     if (lane == 0) lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
@@ -217,13 +208,8 @@ cudaError_t launch_tree_simt(const float *q, const float *kc, const float *vc, f
     const long long ctas = (long long)row_tiles * s.Hkv * s.splits * s.B;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     tree_simt_kernel<<<(unsigned)ctas, 128, 0, st>>>(q, kc, vc, out, lse, ws_o, ws_ml, s, row_tiles);
-    return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t launch_tree_combine(T *out, float *lse, const TreeShape &s, const float *ws_o, const float *ws_ml,
-                                cudaStream_t st)
-{
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || s.splits <= 1) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(((long long)s.max_q * s.Hq + 3) / 4), (unsigned)s.B);
     cfg.blockDim = dim3(128);
@@ -233,12 +219,7 @@ cudaError_t launch_tree_combine(T *out, float *lse, const TreeShape &s, const fl
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<T>, out, lse, ws_o, ws_ml, s);
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel, out, lse, (const float *)ws_o, (const float *)ws_ml, s);
 }
-
-template cudaError_t launch_tree_combine<float>(float *, float *, const TreeShape &, const float *, const float *,
-                                                cudaStream_t);
-template cudaError_t launch_tree_combine<__nv_bfloat16>(__nv_bfloat16 *, float *, const TreeShape &, const float *,
-                                                        const float *, cudaStream_t);
 
 }  // namespace attn_sink

@@ -12,10 +12,18 @@
 // Design: T drafted tokens times G query heads of a KV group share every K/V
 // byte, T G 64 flop a byte: with up to 128 rows a KV head the kernel is bound by
 // HBM, beyond that by the softmax (one exponential per 256 flop).
-//  * CTA = (row tile, KV head, split, sequence); row tiles of one chunk and the
-//    KV heads of one token range are neighbours in the grid, so their K/V rows
-//    meet in L2.  Two CTAs per SM (256 TMEM columns each): one's start, end and
-//    waits hide behind the other's exponentials.
+//  * The work is one line of 64-key tiles, sequence by sequence, cut evenly over
+//    teams of CTAs, whatever the lengths: as many as fit the GPU at once (two CTAs
+//    per SM, 256 TMEM columns each).  A team has a CTA for every row tile and KV
+//    head, which walk the same tokens at the same time, so that row tiles meet in L2 and the
+//    heads' 128-byte rows of a token are read from one DRAM page (with the heads one
+//    after the other on the line, 64 sequences of 8 tokens took 558 us instead of 400);
+//    of groups of KV heads, where all of them would leave too many SMs idle.  A team's
+//    stretch covers a few segments (stretches of one sequence); a segment
+//    that is not the whole of its sequence leaves a partial (m, l, o) in the
+//    workspace, at most two per CTA, and the join kernel adds them up.  (With a grid of
+//    fixed chunks the last wave, the starts and the partials took a third of the time:
+//    16 sequences of 61 tokens 209 us unsplit, 235 in chunks of 2048 keys, 266 in 1024.)
 //  * A row tile is 128 / C rows, held C times in the 128 lanes of the MMA tile
 //    (C = 4, 2, 1 for up to 32, 64, more rows): copy k's threads take the
 //    k-th part of every tile's keys and write zeros of P elsewhere, once, so
@@ -65,34 +73,54 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSumLimit = 1024.f;
 
 constexpr int kTileBytes = kBN * kD * 2;
-constexpr int kRedStride = 67;  // floats a row (copy) of the exchange at the end
 constexpr int kOffQ = 0;
 constexpr int kOffK = kM * kD * 2;
 constexpr int kOffV = kOffK + kNS * kTileBytes;
 constexpr int kOffPath = kOffV + kNS * kTileBytes;         // [128][kPathWords] ancestor bits
 constexpr int kOffDepth = kOffPath + kM * kPathWords * 4;  // [128] depths
 constexpr int kOffPar = kOffDepth + kM * 2;                // [256] parents
-constexpr int kOffBar = kOffPar + kTreeMaxTokens * 2;
-// k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_done, o_last
-constexpr int kNumBar = 4 * kNS + 6;
-constexpr int kOffMisc = kOffBar + kNumBar * 8;  // TMEM address, abort flag
+constexpr int kOffMl = kOffPar + kTreeMaxTokens * 2;       // [128] (m, l) of the copies
+constexpr int kOffBar = kOffMl + kM * 8;
+// k_full[], k_empty[], v_full[], v_empty[], s_full[2], p_full[2], o_done, o_last, q_full
+constexpr int kNumBar = 4 * kNS + 7;
+constexpr int kOffPlan = kOffBar + (kNumBar + 1) / 2 * 16;  // TreeSpan, then the scan's warp sums
+constexpr int kOffMisc = kOffPlan + 32 + 8 * 8;             // TMEM address, abort flag
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
-static_assert(kM * kRedStride * 4 <= kOffPath, "the exchange reuses Q and the K/V ring");
 static_assert(kOffBar % 8 == 0, "barriers on 8 bytes");
 static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
 // tensor memory: S and P (bf16) double-buffered, O
 constexpr int kTmS = 0, kTmP = 2 * kBN, kTmO = kTmP + kBN, kTmCols = 256;
 static_assert(kTmO + kD <= kTmCols && kCtasPerSm * kTmCols <= 512, "tensor memory");
+// shortest stretch of the line; units up to kTreeSnapTiles are never cut
+constexpr int kTreeMinTiles = 4, kTreeSnapTiles = 8;
 
 struct TreeTcParams {
     TreeShape s;
-    int G, row_tiles, box_rows;
+    int G, row_tiles, copies, box_rows;
+    int heads, head_groups;  // KV heads of a team; groups of them (units of the line) per sequence
+    int teams;   // stretches of the line; a team is heads * row_tiles CTAs
+    int q_min;   // shortest stretch, in tiles
+    int snap;    // whole units (sequence, group of KV heads) only: no partials
     float c_log2;
     const __nv_bfloat16 *q;
     __nv_bfloat16 *out;
     float *lse, *ws_o, *ws_ml;
+    long long *plan;  // [0] tiles a stretch, [1 + b] tiles in front of sequence b (B + 1 entries)
     unsigned *status;
     long long timeout_ns;
+};
+
+// tiles of one unit of sequence b: the keys some row of it sees, at least one (a sequence without keys gets
+// its output from a tile that is masked altogether); none without rows
+__device__ __forceinline__ int unit_tiles(const TreeSeq &q)
+{
+    return q.T <= 0 ? 0 : max(1, (q.len - q.lo_al + kBN - 1) / kBN);
+}
+
+// A CTA's stretch [pos, end) of the line, starting in sequence b, which begins at tile base.
+struct TreeSpan {
+    long long pos, end, base;
+    int b;
 };
 
 __device__ __forceinline__ bool wait_noabort(uint64_t *bar, uint32_t parity, unsigned *status, long long tmo)
@@ -133,23 +161,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *k_empty = k_full + kNS, *v_full = k_empty + kNS, *v_empty = v_full + kNS;
     uint64_t *s_full = v_empty + kNS, *p_full = s_full + 2, *o_done = p_full + 2, *o_last = o_done + 1;
+    uint64_t *q_full = o_last + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + kOffMisc + 4);
 
+    long long *scan = reinterpret_cast<long long *>(smem + kOffPlan + 32);
+    TreeSpan *span_s = reinterpret_cast<TreeSpan *>(smem + kOffPlan);
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int rest = blockIdx.x;
-    const int rt = rest % p.row_tiles;
-    rest /= p.row_tiles;
-    const int g = rest % p.s.Hkv;
-    rest /= p.s.Hkv;
-    const int c = rest % p.s.splits, b = rest / p.s.splits;
-    const TreeSeq sq = tree_seq(p.s, b);
-    const int rows = min(sq.T, p.s.max_q) * p.G, r0 = rt * kRows;
-    if (c >= sq.nsplit || r0 >= rows) return;  // uniform over the CTA
-    const int nrow = min(kRows, rows - r0);
-    const int kbeg = sq.lo_al + c * p.s.chunk;
-    const int kend = min((long long)sq.len, (long long)kbeg + p.s.chunk);
-    const int n_tiles = kend > kbeg ? (kend - kbeg + kBN - 1) / kBN : 0;
+    const int rt = blockIdx.x % p.row_tiles, head = blockIdx.x / p.row_tiles % p.heads;
+    const int team = blockIdx.x / p.row_tiles / p.heads, r0 = rt * kRows;
 
     // the first try and its vote keep the warp converged when the phase is over, or ends while the try is
     // suspended; only a try that runs out takes the bounded polling loop
@@ -158,114 +179,153 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         return __all_sync(0xffffffffu, mbar_wait_slow(bar, parity, abort_flag, p.status, p.timeout_ns));
     };
 
-    // ---- producers' state.  A tile's slot in its page is 0 for pages of at most a tile, else it advances with
-    // the tiles; `page` holds the pages of 32 boxes, one a lane, and next_page the 32 after them, loaded a
-    // batch ahead.
-    const int ps = p.s.page_size, nb = kBN / p.box_rows, per = 32 / nb;  // boxes of a tile, tiles of a batch
-    int pt = 0, pst = 0, in_batch = 0, page = 0, next_page = 0;
-    uint32_t pph = 1;
-    int slot = kbeg;
-    auto pages = [&](int t0) -> int {
-        // boxes behind the sequence (masked) reuse its last page, so the table is only read within the
-        // sequence's own entries
-        const int lp = (kbeg + t0 * kBN + lane * p.box_rows) / ps;
-        return p.s.page_table[(size_t)b * p.s.max_pages + min(lp, (sq.len - 1) / ps)];
-    };
-    auto start_pages = [&]() {
-        if (ps == 0 || n_tiles == 0) return;
-        slot = kbeg % ps;
-        page = pages(0);
-        if (per < n_tiles) next_page = pages(per);
-    };
-    // tiles up to t_end into their ring: the whole warp runs the loop, so that every operand is warp-uniform,
-    // and one elected lane issues (from a lane == 0 branch an issue took twice as long)
-    auto produce = [&](const CUtensorMap &map, uint64_t *full, uint64_t *empty, uint32_t ring, int t_end) -> bool {
-        for (; pt < t_end; ++pt) {
-            int outer[kBN / 8];
-            outer[0] = b;
-            if (ps > 0) {
-                if (in_batch == per) {
-                    in_batch = 0;
-                    page = next_page;
-                    if (pt + per < n_tiles) next_page = pages(pt + per);
-                }
+    // ---- the plan: every CTA scans the batch's lengths (a thread a run of sequences) and takes its stretch
+    TreeSpan span;
+    {
+        const int run = (p.s.B + kThreads - 1) / kThreads;
+        const int b0 = min((int)threadIdx.x * run, p.s.B), b1 = min(b0 + run, p.s.B);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += (long long)unit_tiles(tree_seq(p.s, b)) * p.head_groups;
+        long long incl = mine;
 #pragma unroll
-                for (int i = 0; i < kBN / 8; ++i)
-                    if (i < nb) outer[i] = __shfl_sync(0xffffffffu, page, in_batch * nb + i);
-                ++in_batch;
-            }
-            if (!wait_all(&empty[pst], pph)) return false;
-            if (elect_one()) {
-                const uint32_t dst = ring + pst * kTileBytes, bar = smem_u32(&full[pst]);
-                mbar_arrive_expect_tx(&full[pst], kTileBytes);
-                tma_load_4d_at(dst, &map, 0, g, slot, outer[0], bar);
-#pragma unroll
-                for (int i = 1; i < kBN / 8; ++i)
-                    if (i < nb) tma_load_4d_at(dst + i * p.box_rows * kD * 2, &map, 0, g, slot, outer[i], bar);
-            }
-            __syncwarp();
-            if (ps == 0 || ps > kBN) {
-                slot += kBN;
-                if (slot == ps) slot = 0;
-            }
-            if (++pst == kNS) {
-                pst = 0;
-                pph ^= 1u;
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
         }
-        return true;
+        if (lane == 31) scan[warp] = incl;
+        if (threadIdx.x == 0) span_s->b = -1;
+        __syncthreads();
+        long long before = incl - mine, total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += scan[w];
+            total += scan[w];
+        }
+        const long long q = max((total + p.teams - 1) / p.teams, (long long)p.q_min);
+        const long long first = q * team, last = min(first + q, total);
+        // (snap: the units that start in [first, last), whole)
+        long long at = before;
+        for (int b = b0; b < b1; ++b) {
+            const int nt = unit_tiles(tree_seq(p.s, b));
+            const long long len = (long long)nt * p.head_groups;
+            if (blockIdx.x == 0 && p.plan) p.plan[1 + b] = at;
+            if (first < last && at <= first && first < at + len) {
+                span_s->pos = p.snap ? at + (first - at + nt - 1) / nt * nt : first;
+                span_s->end = last;
+                span_s->base = at;
+                span_s->b = b;
+            }
+            at += len;
+        }
+        if (blockIdx.x == 0 && p.plan && b1 == p.s.B && b0 < b1) {
+            p.plan[0] = q;
+            p.plan[1 + p.s.B] = total;
+        }
+        __syncthreads();
+        span = *span_s;
+        if (span.b < 0) return;  // no work: uniform over the CTA
+    }
+    // segment by segment: f(sequence, its number, KV head, first tile, tiles, all tiles of the unit); stops at false
+    auto for_segments = [&](auto f) {
+        long long pos = span.pos, base = span.base;
+        int b = span.b;
+        TreeSeq sq = tree_seq(p.s, b);
+        int nt = unit_tiles(sq);
+        while (pos < span.end) {
+            while (pos >= base + (long long)nt * p.head_groups) {
+                base += (long long)nt * p.head_groups;
+                sq = tree_seq(p.s, ++b);
+                nt = unit_tiles(sq);
+            }
+            const int g = (int)((pos - base) / nt) * p.heads + head, ta = (int)((pos - base) % nt);
+            const int n = p.snap ? nt : (int)min((long long)(nt - ta), span.end - pos);
+            if (r0 < min(sq.T, p.s.max_q) * p.G && !f(sq, b, g, ta, n, nt, pos == span.pos)) return;
+            pos += n;
+        }
     };
-    // every load issued must land before the CTA may exit
-    auto drain = [&](uint64_t *full) {
+
+    // ---- producers.  The whole warp runs the loop, so that every operand is warp-uniform, and one elected
+    // lane issues (from a lane == 0 branch an issue took twice as long).
+    int pt = 0;  // tiles issued
+    auto produce = [&](const CUtensorMap &map, uint64_t *full, uint64_t *empty, uint32_t ring) {
+        const int ps = p.s.page_size, nb = kBN / p.box_rows, per = 32 / nb;  // boxes of a tile, tiles of a batch
+        int st = 0;
+        uint32_t ph = 1;
+        if (elect_one()) tma_prefetch_desc(&map);
+        for_segments([&](const TreeSeq &sq, int b, int g, int ta, int n, int, bool) -> bool {
+            const int key0 = sq.lo_al + ta * kBN;
+            // the pages of 32 boxes from tile t of the segment on, one a lane; boxes behind the sequence
+            // (masked) reuse its last page, so the table is only read within the sequence's own entries
+            auto pages = [&](int t) -> int {
+                const int lp = (key0 + t * kBN + lane * p.box_rows) / ps;
+                return p.s.page_table[(size_t)b * p.s.max_pages + min(lp, max(sq.len - 1, 0) / ps)];
+            };
+            // a tile's slot in its page: 0 for pages of at most a tile, else it advances with the tiles
+            int slot = ps > 0 ? key0 % ps : key0, in_batch = 0;
+            int page = 0, next_page = 0;
+            if (ps > 0) {
+                page = pages(0);
+                if (per < n) next_page = pages(per);
+            }
+            for (int t = 0; t < n; ++t) {
+                int outer[kBN / 8];
+                outer[0] = b;
+                if (ps > 0) {
+                    if (in_batch == per) {
+                        in_batch = 0;
+                        page = next_page;  // loaded a batch ahead
+                        if (t + per < n) next_page = pages(t + per);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kBN / 8; ++i)
+                        if (i < nb) outer[i] = __shfl_sync(0xffffffffu, page, in_batch * nb + i);
+                    ++in_batch;
+                }
+                if (!wait_all(&empty[st], ph)) return false;
+                if (elect_one()) {
+                    const uint32_t dst = ring + st * kTileBytes, bar = smem_u32(&full[st]);
+                    mbar_arrive_expect_tx(&full[st], kTileBytes);
+                    tma_load_4d_at(dst, &map, 0, g, slot, outer[0], bar);
+#pragma unroll
+                    for (int i = 1; i < kBN / 8; ++i)
+                        if (i < nb) tma_load_4d_at(dst + i * p.box_rows * kD * 2, &map, 0, g, slot, outer[i], bar);
+                }
+                __syncwarp();
+                if (ps == 0 || ps > kBN) {
+                    slot += kBN;
+                    if (slot == ps) slot = 0;
+                }
+                ++pt;
+                if (++st == kNS) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            return true;
+        });
+        // every load issued must land before the CTA may exit
         for (int x = 0; x < kNS && x < pt; ++x)
             wait_noabort(&full[x], (uint32_t)((pt - 1 - x) / kNS) & 1u, p.status, p.timeout_ns);
     };
 
-    // ---- start: what needs no other warp, side by side
-    const int lrow = warp * 32 + lane;                // softmax warps: TMEM lane
-    const int r = lrow % kRows, copy = lrow / kRows;  // row of the tile, copy of it
-    const bool valid = warp < 4 && r < nrow;
-    const int row = r0 + (valid ? r : 0);
-    const int i0 = r0 / p.G, tok = row / p.G - i0, h = g * p.G + row % p.G;
-    const size_t at = (size_t)(sq.row0 + row / p.G) * p.s.Hq + h;
-    uint32_t(*path)[kPathWords] = reinterpret_cast<uint32_t(*)[kPathWords]>(smem + kOffPath);
-    int16_t *depth = reinterpret_cast<int16_t *>(smem + kOffDepth);
-    if (warp < 4) {
-        // Q: this thread's row into the 128-byte-swizzled operand tile (rows that do not exist: zeros)
-        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * kD);
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = valid ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4 *>(smem + kOffQ + lrow * 128 + ((k ^ (lrow & 7)) << 4)) = v[k];
-        fence_proxy_async_smem();
-        if (p.s.window > 0 || kend > sq.cached)
-            tree_paths(p.s, sq, i0, (r0 + nrow - 1) / p.G - i0 + 1, lrow, 128,
-                       reinterpret_cast<int16_t *>(smem + kOffPar), path, depth, [] { named_bar_sync(1, 128); });
-    } else if (warp == 4) {
-        if (lane == 0) {
-            for (int i = 0; i < kNS; ++i) {
-                mbar_init(&k_full[i], 1);
-                mbar_init(&k_empty[i], 1);
-                mbar_init(&v_full[i], 1);
-                mbar_init(&v_empty[i], 1);
-            }
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&s_full[i], 1);
-                mbar_init(&p_full[i], 4);  // the softmax warps
-            }
-            mbar_init(o_done, 1);
-            mbar_init(o_last, 1);
-            *abort_flag = 0;
-            fence_mbar_init();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kNS; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
         }
-        __syncwarp();
-        start_pages();
-        produce(tmK, k_full, k_empty, smem_u32(smem + kOffK), min(n_tiles, kNS));  // (the ring is empty)
-    } else if (warp == 5) {
-        start_pages();
-    } else {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);  // the softmax warps
+        }
+        mbar_init(o_done, 1);
+        mbar_init(o_last, 1);
+        mbar_init(q_full, 4);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 6) {
         tmem_alloc(tmem_slot, kTmCols);
         tmem_relinquish();
     }
@@ -275,100 +335,107 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const uint32_t tmem = *tmem_slot;
 
     if (warp == 4) {
-        produce(tmK, k_full, k_empty, smem_u32(smem + kOffK), n_tiles);
-        drain(k_full);
+        produce(tmK, k_full, k_empty, smem_u32(smem + kOffK));
     } else if (warp == 5) {
-        produce(tmV, v_full, v_empty, smem_u32(smem + kOffV), n_tiles);
-        drain(v_full);
+        produce(tmV, v_full, v_empty, smem_u32(smem + kOffV));
     } else if (warp == 6) {
         // ------------------------------------------------------------ MMA issuer (converged, one lane issues)
         constexpr uint32_t id_s = idesc_bf16_f32(kM, kBN, 0), id_pv = idesc_bf16_f32(kM, kD, 1);
         const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
         const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
         const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + kOffV), kBN * 128, 1024);
-        int kt = 0, kst = 0;  // next tile of S, its stage and phase
-        uint32_t kph = 0;
+        int kst = 0, st = 0;  // stages of the next K, of the next V, and their phases
+        uint32_t kph = 0, ph = 0;
+        uint32_t sn = 0, n_seg = 0;            // tiles of S so far; segments
+        bool pending = false;                  // products issued that no o_last covers
         auto issue_s = [&]() {  // one lane
             const uint64_t kd = k_desc + (uint64_t)((uint32_t)(kst * kTileBytes) >> 4);
-            const uint32_t ts = tmem + kTmS + (kt & 1) * kBN;
+            const uint32_t ts = tmem + kTmS + (sn & 1) * kBN;
 #pragma unroll
             for (int kk = 0; kk < kD / 16; ++kk)
                 mma_ss(ts, q_desc + (uint64_t)(kk * 32 >> 4), kd + (uint64_t)(kk * 32 >> 4), id_s, kk > 0 ? 1u : 0u);
-            mma_commit(&s_full[kt & 1]);
+            mma_commit(&s_full[sn & 1]);
             mma_commit(&k_empty[kst]);
         };
         auto next_k = [&]() {
-            ++kt;
+            ++sn;
             if (++kst == kNS) {
                 kst = 0;
                 kph ^= 1u;
             }
         };
-        bool ok = true;
-        while (ok && kt < min(n_tiles, 2)) {
-            ok = wait_all(&k_full[kst], kph);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) issue_s();
-            __syncwarp();
-            next_k();
-        }
-        int st = 0, t = 0;
-        uint32_t ph = 0;
-        for (; ok && t < n_tiles; ++t) {
-            // before P is there: the waits for this V and the K after the next, V's zeros
-            const bool more = kt < n_tiles;
-            if (!wait_all(&v_full[st], ph) || (more && !wait_all(&k_full[kst], kph))) break;
-            const int j0 = kbeg + t * kBN;
-            if (j0 < sq.lo || j0 + kBN > sq.len) {
-                // value rows no row sees may hold anything (0 x NaN is NaN): zeros
-                uint4 *vt = reinterpret_cast<uint4 *>(smem + kOffV + st * kTileBytes);
-                for (int e = lane; e < kBN * 8; e += 32) {
-                    const int j = j0 + (e >> 3);
-                    if (j < sq.lo || j >= sq.len) vt[e] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_proxy_async_smem();
+        uint32_t n = 0;  // tiles of P V so far
+        for_segments([&](const TreeSeq &sq, int, int, int ta, int nt, int, bool) -> bool {
+            if (!wait_all(q_full, n_seg & 1u)) return false;
+            int ahead = 0;  // tiles of this segment with S issued
+            for (; ahead < min(nt, 2); ++ahead) {
+                if (!wait_all(&k_full[kst], kph)) return false;
+                tc_fence_after();
+                if (elect_one()) issue_s();
                 __syncwarp();
+                pending = true;
+                next_k();
             }
-            if (!wait_all(&p_full[t & 1], (uint32_t)(t >> 1) & 1u)) break;
-            tc_fence_after();
-            if (elect_one()) {
-                const uint64_t vd = v_desc + (uint64_t)((uint32_t)(st * kTileBytes) >> 4);
-                const uint32_t tp = tmem + kTmP + (t & 1) * (kBN / 2);
+            for (int t = 0; t < nt; ++t, ++n) {
+                // before P is there: the waits for this V and the K after the next, V's zeros
+                const bool more = ahead < nt;
+                if (!wait_all(&v_full[st], ph) || (more && !wait_all(&k_full[kst], kph))) return false;
+                const int j0 = sq.lo_al + (ta + t) * kBN;
+                if (j0 < sq.lo || j0 + kBN > sq.len) {
+                    // value rows no row sees may hold anything (0 x NaN is NaN): zeros
+                    uint4 *vt = reinterpret_cast<uint4 *>(smem + kOffV + st * kTileBytes);
+                    for (int e = lane; e < kBN * 8; e += 32) {
+                        const int j = j0 + (e >> 3);
+                        if (j < sq.lo || j >= sq.len) vt[e] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                // (the first P of a segment: O of the one before has been read, too)
+                if (!wait_all(&p_full[n & 1], (n >> 1) & 1u)) return false;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint64_t vd = v_desc + (uint64_t)((uint32_t)(st * kTileBytes) >> 4);
+                    const uint32_t tp = tmem + kTmP + (n & 1) * (kBN / 2);
 #pragma unroll
-                for (int kk = 0; kk < kBN / 16; ++kk)
-                    mma_ts(tmem + kTmO, tp + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), id_pv,
-                           (t > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(o_done);
-                mma_commit(&v_empty[st]);
-                if (more) issue_s();  // P(t) being there, S(t) has been read
-                // last of all: once o_last is over, no arrival on this CTA's barriers is still to come
-                if (t == n_tiles - 1) mma_commit(o_last);
+                    for (int kk = 0; kk < kBN / 16; ++kk)
+                        mma_ts(tmem + kTmO, tp + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), id_pv,
+                               (t > 0 || kk > 0) ? 1u : 0u);
+                    mma_commit(o_done);
+                    mma_commit(&v_empty[st]);
+                    if (more) issue_s();  // P(t) being there, S(t) has been read
+                    // last of all: once the last o_last is over, no arrival on this CTA's barriers is to come
+                    if (t == nt - 1) mma_commit(o_last);
+                }
+                __syncwarp();
+                if (more) {
+                    next_k();
+                    ++ahead;
+                }
+                if (++st == kNS) {
+                    st = 0;
+                    ph ^= 1u;
+                }
             }
-            __syncwarp();
-            if (more) next_k();
-            if (++st == kNS) {
-                st = 0;
-                ph ^= 1u;
-            }
-        }
+            ++n_seg;
+            pending = false;
+            return true;
+        });
         // given up half way: what is in flight must still end before tensor memory is freed (nobody else
         // waits for o_last then)
-        if (kt > 0 && t < n_tiles) {
+        if (pending) {
             if (elect_one()) mma_commit(o_last);
             __syncwarp();
+            ++n_seg;
         }
-        if (kt > 0) wait_noabort(o_last, 0, p.status, p.timeout_ns);
+        if (n_seg > 0) wait_noabort(o_last, (n_seg - 1) & 1u, p.status, p.timeout_ns);
     } else {
         // ------------------------------------------------------------ softmax + epilogue
-        const bool active = (warp * 32) % kRows < nrow;  // some row of this warp exists
+        const int lrow = warp * 32 + lane;                // TMEM lane
+        const int r = lrow % kRows, copy = lrow / kRows;  // row of the tile, copy of it
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-        const float sink2 = p.s.sinks[h] * kLog2e;
-        // reference maximum in log2 units, a whole number: next to the sink's until a tile moves it
-        float m = rintf(sink2);
-        float l = 0.f;   // running sum, without the sink
-        int vis_lo = 0;  // first cached key this row sees
-        if (p.s.window > 0) vis_lo = max(0, sq.cached + depth[tok] - p.s.window + 1);
+        uint32_t(*path)[kPathWords] = reinterpret_cast<uint32_t(*)[kPathWords]>(smem + kOffPath);
+        int16_t *depth = reinterpret_cast<int16_t *>(smem + kOffDepth);
         if (C > 1) {
             // P of the keys of the other copies stays zero
             uint32_t z[16];
@@ -378,12 +445,44 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int k = 0; k < kBN / 16; ++k) tmem_st16(trow + kTmP + 16 * k, z);
         }
         const float2 C2 = make_float2(p.c_log2, p.c_log2);
+        uint32_t n = 0, n_seg = 0;  // tiles, segments so far
+        for_segments([&](const TreeSeq &sq, int, int g, int ta, int nt, int nt_unit, bool is_first) -> bool {
+        const int rows = min(sq.T, p.s.max_q) * p.G, nrow = min(kRows, rows - r0);
+        const bool valid = r < nrow;
+        const bool active = (warp * 32) % kRows < nrow;  // some row of this warp exists
+        const int row = r0 + (valid ? r : 0);
+        const int i0 = r0 / p.G, tok = row / p.G - i0, h = g * p.G + row % p.G;
+        const size_t at = (size_t)(sq.row0 + row / p.G) * p.s.Hq + h;
+        {
+            // Q: this thread's row into the 128-byte-swizzled operand tile (rows that do not exist: zeros)
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * kD);
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = valid ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4 *>(smem + kOffQ + lrow * 128 + ((k ^ (lrow & 7)) << 4)) = v[k];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        }
+        const int kfirst = sq.lo_al + ta * kBN;  // first key of the segment
+        const float sink2 = p.s.sinks[h] * kLog2e;
+        // reference maximum in log2 units, a whole number: next to the sink's until a tile moves it
+        float m = rintf(sink2);
+        float l = 0.f;   // running sum, without the sink
+        int vis_lo = 0;  // first cached key this row sees
+        if (p.s.window > 0 || kfirst + nt * kBN > sq.cached) {
+            tree_paths(p.s, sq, i0, (r0 + nrow - 1) / p.G - i0 + 1, lrow, 128,
+                       reinterpret_cast<int16_t *>(smem + kOffPar), path, depth, [] { named_bar_sync(1, 128); });
+            if (p.s.window > 0) vis_lo = max(0, sq.cached + depth[tok] - p.s.window + 1);
+        }
         bool ok = true;
-        for (int t = 0; t < n_tiles; ++t) {
-            const int sb = t & 1;
-            const int j0 = kbeg + t * kBN;
+        for (int t = 0; t < nt; ++t, ++n) {
+            const int sb = n & 1;
+            const int j0 = kfirst + t * kBN;
             // S(t) is complete, and with it P V(t - 2): this P buffer is free
-            if (!wait_all(&s_full[sb], (uint32_t)(t >> 1) & 1u)) {
+            if (!wait_all(&s_full[sb], (n >> 1) & 1u)) {
                 ok = false;
                 break;
             }
@@ -451,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (t > 0) {
                         // O must hold the tile before, too.  (P V(t - 2) is complete, P V(t) not issued:
                         // the parity is unambiguous although other phases go unobserved.)
-                        if (!wait_all(o_done, (uint32_t)(t - 1) & 1u)) {
+                        if (!wait_all(o_done, (n - 1) & 1u)) {
                             ok = false;
                             break;
                         }
@@ -474,25 +573,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             __syncwarp();
             if (lane == 0) mbar_arrive(&p_full[sb]);
         }
-        const bool any = n_tiles > 0;
-        if (ok && active && any) ok = wait_all(o_last, 0);
         // -------------------------------------------------------- epilogue
+        // (every warp waits: Q, which S reads, is free then, too)
+        ok = ok && wait_all(o_last, n_seg & 1u);
+        ++n_seg;
         tc_fence_after();
-        // 16 columns of O
-        auto load_o = [&](int k, float (&o)[16]) {
-            uint32_t x[16];
-            if (any) {
-                tmem_ld16(trow + kTmO + 16 * k, x);
-                tmem_wait_ld();
-            }
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = any ? __uint_as_float(x[e]) : 0.f;
-        };
-        const size_t part = at * p.s.splits + c;
+        const bool whole = nt == nt_unit;
+        // a segment of a unit leaves a partial: the CTA's first segment in its first slot, its last in the second
+        const size_t part = ((size_t)blockIdx.x * 2 + (is_first ? 0 : 1)) * kRows + r;
         float L = l, scale_o = 1.f;
-        // the row's statistics are final: a partial of its split, or the sink's share and the norm
+        // the row's statistics are final: a partial, or the sink's share and the norm
         auto finish_row = [&](bool write) {
-            if (sq.nsplit > 1) {
+            if (!whole) {
                 if (write) *reinterpret_cast<float2 *>(p.ws_ml + part * 2) = make_float2(m, L);
                 return;
             }
@@ -503,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         };
         // 8 columns of the row from column d on
         auto store_o = [&](int d, const float *o) {
-            if (sq.nsplit > 1) {
+            if (!whole) {
                 float4 *dst = reinterpret_cast<float4 *>(p.ws_o + part * kD + d);
                 dst[0] = make_float4(o[0], o[1], o[2], o[3]);
                 dst[1] = make_float4(o[4], o[5], o[6], o[7]);
@@ -512,6 +604,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     make_uint4(pack_bf16x2(o[0] * scale_o, o[1] * scale_o), pack_bf16x2(o[2] * scale_o, o[3] * scale_o),
                                pack_bf16x2(o[4] * scale_o, o[5] * scale_o), pack_bf16x2(o[6] * scale_o, o[7] * scale_o));
             }
+        };
+        auto load_o = [&](int k, float (&o)[16]) {  // 16 columns of O
+            uint32_t x[16];
+            tmem_ld16(trow + kTmO + 16 * k, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(x[e]);
         };
         if (C == 1) {
             if (ok && active) {
@@ -527,55 +626,62 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
             }
         } else {
-            // The copies of a row join through Q and the ring, which are free (every product, and so every load
-            // it read, has completed); thread (row, copy) takes the copy-th part of the columns.  The barrier
-            // is reached by all 128 threads, after an expired wait too.
-            constexpr int kOut = kD / C;
-            float *red = reinterpret_cast<float *>(smem);
+            // The copies of a row join through Q's buffer, 32 columns at a time (element c of a row at c ^ row:
+            // no bank conflicts); thread (row, copy) takes the copy-th part of them.  The barriers are
+            // reached by all 128 threads, after an expired wait too.
+            float *red = reinterpret_cast<float *>(smem + kOffQ);
+            float2 *ml = reinterpret_cast<float2 *>(smem + kOffMl);
             if (!ok) *abort_flag = 1;
-            if (ok && active) {
-                float *me = red + lrow * kRedStride;
+            ml[lrow] = make_float2(m, l);
+            float f[C];
 #pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                    float o[16];
-                    load_o(k, o);
+            for (int half = 0; half < 2; ++half) {
+                if (ok && active) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) me[16 * k + e] = o[e];
+                    for (int k = 0; k < 2; ++k) {
+                        float o[16];
+                        load_o(2 * half + k, o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) red[lrow * 32 + ((16 * k + e) ^ lane)] = o[e];
+                    }
                 }
-                me[kD] = m;
-                me[kD + 1] = l;
-            }
-            named_bar_sync(1, 128);
-            if (*abort_flag == 0 && valid) {
-                const float *you = red + r * kRedStride;  // copy k: k * kRows rows on
-                float f[C];
-                m = -INFINITY;
+                named_bar_sync(1, 128);
+                if (*abort_flag == 0 && valid) {
+                    if (half == 0) {
+                        m = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < C; ++k) {
-                    f[k] = you[k * kRows * kRedStride + kD];
-                    m = fmaxf(m, f[k]);
+                        for (int k = 0; k < C; ++k) {
+                            f[k] = ml[k * kRows + r].x;
+                            m = fmaxf(m, f[k]);
+                        }
+                        L = 0.f;
+#pragma unroll
+                        for (int k = 0; k < C; ++k) {
+                            f[k] = f[k] == -INFINITY ? 0.f : ex2(f[k] - m);
+                            L = fmaf(f[k], ml[k * kRows + r].y, L);
+                        }
+                        finish_row(copy == 0);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 32 / C / 8; ++x) {
+                        const int d = copy * (32 / C) + 8 * x;
+                        float o[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll
+                        for (int k = 0; k < C; ++k)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                o[e] = fmaf(f[k], red[(k * kRows + r) * 32 + ((d + e) ^ (r & 31))], o[e]);
+                        store_o(32 * half + d, o);
+                    }
                 }
-                L = 0.f;
-#pragma unroll
-                for (int k = 0; k < C; ++k) {
-                    f[k] = f[k] == -INFINITY ? 0.f : ex2(f[k] - m);
-                    L = fmaf(f[k], you[k * kRows * kRedStride + kD + 1], L);
-                }
-                finish_row(copy == 0);
-#pragma unroll
-                for (int x = 0; x < kOut / 8; ++x) {
-                    const int d = copy * kOut + 8 * x;
-                    float o[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = 0.f;
-#pragma unroll
-                    for (int k = 0; k < C; ++k)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = fmaf(f[k], you[k * kRows * kRedStride + d + e], o[e]);
-                    store_o(d, o);
-                }
+                named_bar_sync(1, 128);
             }
         }
+        // all 128 threads go on or none does: the next segment has barriers among them
+        return !named_bar_or(1, 128, !ok);
+        });
     }
 
     tc_fence_before();
@@ -589,25 +695,136 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
 }  // namespace
 
-cudaError_t launch_tree_tc(const void *q, const void *kc, const void *vc, void *out, float *lse, const TreeShape &s,
-                           float *ws_o, float *ws_ml, cudaStream_t st)
+namespace {
+
+// One warp per (token, query head) of sequence blockIdx.y, for units that were cut: M = max(sink, max_c m_c),
+// L = 2^(sink - M) + sum_c l_c 2^(m_c - M), o = sum_c 2^(m_c - M) o_c / L, the pieces in the order of their keys.
+__global__ void __launch_bounds__(128) tree_join_kernel(const TreeTcParams p)
 {
+    grid_dep_wait();  // the partials and the plan of the grid ahead (programmatic dependent launch)
+    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int w = blockIdx.x * 4 + (threadIdx.x >> 5);  // (token, head) of the sequence
+    const SeqRows sr = seq_rows(p.s.cu_q, b, 0, p.s.total_q);
+    if (w >= min(sr.len, p.s.max_q) * p.s.Hq) return;
+    const int h = w % p.s.Hq, g = h / p.G, row = w / p.s.Hq * p.G + h % p.G;
+    const int per_tile = kM / p.copies, rt = row / per_tile, r = row % per_tile;
+    const long long q = p.plan[0], base = p.plan[1 + b], nt = (p.plan[2 + b] - base) / p.head_groups;
+    const long long u0 = base + g / p.heads * nt;                      // the unit's first tile
+    const int j0 = (int)(u0 / q), j1 = (int)((u0 + nt - 1) / q);  // the teams it was cut over
+    if (j0 == j1) return;  // written in one piece
+    auto slot = [&](int j) -> size_t {
+        const int second = j == j0 && u0 % q != 0;  // not the first segment of its CTA
+        return ((size_t)((j * p.heads + g % p.heads) * p.row_tiles + rt) * 2 + second) * per_tile + r;
+    };
+    const float sk = p.s.sinks[h] * kLog2e;
+    float M = sk;
+    for (int j = j0 + lane; j <= j1; j += 32) M = fmaxf(M, p.ws_ml[slot(j) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.f;
+    float2 acc = make_float2(0.f, 0.f);
+    for (int jb = j0; jb <= j1; jb += 32) {
+        float f = 0.f;  // weight of piece jb + lane
+        if (jb + lane <= j1) {
+            const float2 ml = *reinterpret_cast<const float2 *>(p.ws_ml + slot(jb + lane) * 2);
+            f = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
+            L = fmaf(f, ml.y, L);
+        }
+        const int n = min(32, j1 - jb + 1);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k);
+            const float2 o = reinterpret_cast<const float2 *>(p.ws_o + slot(jb + k) * kD)[lane];
+            acc.x = fmaf(fk, o.x, acc.x);
+            acc.y = fmaf(fk, o.y, acc.y);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    L += sk == -INFINITY ? 0.f : ex2(sk - M);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const size_t at = (size_t)sr.row0 * p.s.Hq + w;
+    reinterpret_cast<uint32_t *>(p.out + at * kD)[lane] = pack_bf16x2(acc.x * inv, acc.y * inv);
+    if (lane == 0) p.lse[at] = L > 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+// How the line is cut, from what the host knows.
+struct TreePlan {
+    int copies, row_tiles, heads, teams, q_min, snap;
+    size_t plan_bytes, ml_floats, o_floats;
+};
+TreePlan tree_plan(const TreeShape &s, int num_splits)
+{
+    TreePlan t;
+    const long long rows = (long long)s.max_q * (s.Hq / s.Hkv);
+    t.copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+    t.row_tiles = (int)((rows * t.copies + kM - 1) / kM);
+    // tiles of the longest possible unit
+    const long long lw = s.window > 0 ? (long long)s.window - 1 + s.max_q + kBN - 1 : (long long)s.Lmax;
+    const long long most = ((lw < s.Lmax ? lw : s.Lmax) + kBN - 1) / kBN;
+    t.snap = num_splits == 0 && most <= kTreeSnapTiles;
+    // all KV heads in a team, or the largest part of them that keeps nine SMs of ten busy
+    const int fit = 148 * kCtasPerSm;
+    t.heads = 1;
+    for (int h = s.Hkv; h >= 1; --h) {
+        const long long team = (long long)h * t.row_tiles;
+        if (s.Hkv % h == 0 && team <= fit && fit / team * team * 10 >= fit * 9) {
+            t.heads = h;
+            break;
+        }
+    }
+    const long long line = most * (s.Hkv / t.heads) * s.B;
+    long long teams = fit / ((long long)t.heads * t.row_tiles);
+    t.q_min = kTreeMinTiles;
+    if (num_splits > 0) {
+        t.q_min = (int)((most + num_splits - 1) / num_splits);
+        teams = (line + t.q_min - 1) / t.q_min;
+        const long long cap = 4096 / t.heads;  // (the stretches are then longer)
+        if (teams > cap) teams = cap;
+    }
+    const long long useful = t.snap ? line : (line + t.q_min - 1) / t.q_min;
+    if (teams > useful) teams = useful;
+    t.teams = (int)(teams < 1 ? 1 : teams);
+    const size_t slots = t.snap ? 0 : (size_t)t.teams * t.heads * t.row_tiles * 2 * (kM / t.copies);
+    t.plan_bytes = t.snap ? 0 : ((size_t)s.B + 2) * 8 + 15 & ~(size_t)15;
+    t.ml_floats = slots * 2;
+    t.o_floats = slots * kD;
+    return t;
+}
+
+}  // namespace
+
+size_t tree_tc_workspace_bytes(const TreeShape &s, int num_splits)
+{
+    const TreePlan t = tree_plan(s, num_splits);
+    return t.plan_bytes + (t.ml_floats + t.o_floats) * sizeof(float);
+}
+
+cudaError_t launch_tree_tc(const void *q, const void *kc, const void *vc, void *out, float *lse, const TreeShape &s,
+                           int num_splits, void *ws, cudaStream_t st)
+{
+    const TreePlan t = tree_plan(s, num_splits);
     TreeTcParams p;
     p.s = s;
     p.G = s.Hq / s.Hkv;
-    const long long rows = (long long)s.max_q * p.G;
-    const int copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-    p.row_tiles = (int)((rows * copies + kM - 1) / kM);
+    p.copies = t.copies;
+    p.row_tiles = t.row_tiles;
+    p.heads = t.heads;
+    p.head_groups = s.Hkv / t.heads;
+    p.teams = t.teams;
+    p.q_min = t.q_min;
+    p.snap = t.snap;
     p.box_rows = s.page_size > 0 && s.page_size < kBN ? s.page_size : kBN;
     p.c_log2 = s.scale * kLog2e;
     p.q = static_cast<const __nv_bfloat16 *>(q);
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
-    p.ws_o = ws_o;
-    p.ws_ml = ws_ml;
+    p.plan = t.snap ? nullptr : static_cast<long long *>(ws);
+    p.ws_o = t.snap ? nullptr : reinterpret_cast<float *>(static_cast<char *>(ws) + t.plan_bytes);
+    p.ws_ml = t.snap ? nullptr : p.ws_o + t.o_floats;
     p.status = device_status_ptr();
     p.timeout_ns = wait_timeout_ns();
-    const long long ctas = (long long)p.row_tiles * s.Hkv * s.splits * s.B;
+    const long long ctas = (long long)t.teams * t.heads * t.row_tiles;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     alignas(64) CUtensorMap mk, mv;
     // contiguous: [B][Lmax][Hkv][64]; paged pool: [num_pages][page_size][Hkv][64]
@@ -619,11 +836,22 @@ cudaError_t launch_tree_tc(const void *q, const void *kc, const void *vc, void *
     if (!encode_tensor_map_4d(&mk, const_cast<void *>(kc), 2, dims, strides, box, true) ||
         !encode_tensor_map_4d(&mv, const_cast<void *>(vc), 2, dims, strides, box, true))
         return cudaErrorInvalidValue;
-    auto kern = copies == 4 ? tree_tc_kernel<4> : copies == 2 ? tree_tc_kernel<2> : tree_tc_kernel<1>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    auto kern = t.copies == 4 ? tree_tc_kernel<4> : t.copies == 2 ? tree_tc_kernel<2> : tree_tc_kernel<1>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)ctas, kThreads, kSmemBytes, st>>>(mk, mv, p);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if (e != cudaSuccess || t.snap) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((long long)s.max_q * s.Hq + 3) / 4), (unsigned)s.B);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_join_kernel, p);
 }
 
 }  // namespace attn_sink

@@ -365,7 +365,8 @@ ATTN_SINK_API size_t attn_sink_decode_paged_workspace_size(int B, int Hq, int D,
  *            are not computed, and their rows left as they were.
  *   sinks, window, scale: as attn_sink_fwd (scale positive and finite for
  *            BF16).  dtype F32 (exact) or BF16 (tensor cores); any Hq % Hkv == 0.
- *   num_splits  0 = choose automatically, else 1..128 chunks of the visible keys
+ *   num_splits  0 = cut the batch's work evenly over the GPU; else 1..128: in pieces
+ *            of 1/num_splits of the longest visible range (results differ in rounding only)
  *   workspace  device scratch of attn_sink_decode_tree_workspace_size() bytes
  *            for the same sizes (may be NULL when that is 0); its contents on
  *            entry do not matter.  Calls that may run at once need their own.
@@ -393,8 +394,9 @@ ATTN_SINK_API int attn_sink_decode_tree_paged(const void *q, const void *k_pages
                      void *workspace, size_t ws_bytes, int dtype, void *stream);
 
 /* Bytes of workspace of the two calls above (Lmax = max_pages_per_seq *
- * page_size for a paged cache; 0 when a single split suffices, or for sizes
- * that the calls refuse). */
+ * page_size for a paged cache; 0 when nothing is ever cut, or for sizes that
+ * the calls refuse).  It does not depend on the lengths; a workspace for larger
+ * B, total_q, max_seqlen_q or Lmax need not suffice for smaller ones. */
 ATTN_SINK_API size_t attn_sink_decode_tree_workspace_size(int B, int total_q, int max_seqlen_q, int Hq,
                      int Hkv, int D, int Lmax, int window, int num_splits, int dtype);
 

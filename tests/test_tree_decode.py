@@ -188,14 +188,22 @@ def test_host_checks():
     assert call(q_=q + 8) == MISALIGNED
     assert call(par_=par + 4) == MISALIGNED
     assert call(w=ws + 4) == MISALIGNED
-    need = attn.attn_sink_decode_tree_workspace_size(4, 32, 8, 8, 2, 64, 4096, 0, 8, 1)
-    assert need == 32 * 8 * 8 * 66 * 4  # 8 chunks of 512 keys
+    size = attn.attn_sink_decode_tree_workspace_size
+    need = size(4, 32, 8, 8, 2, 64, 4096, 0, 8, 1)
+    assert need > 0
     assert call(w=None) == WORKSPACE
     assert call(wbytes=need - 1) == WORKSPACE
-    # one split needs none; sizes that the calls refuse report none
-    assert attn.attn_sink_decode_tree_workspace_size(4, 32, 8, 8, 2, 64, 4096, 0, 1, 1) == 0
-    assert attn.attn_sink_decode_tree_workspace_size(4, 32, 257, 8, 2, 64, 4096, 0, 8, 1) == 0
-    assert attn.attn_sink_decode_tree_workspace_size(4, 32, 8, 8, 2, 64, 4096, 0, 129, 1) == 0
+    # fp32: 8 chunks of 512 keys; one chunk needs none
+    assert size(4, 32, 8, 8, 2, 64, 4096, 0, 8, 0) == 32 * 8 * 8 * 66 * 4
+    assert call(dtype=0, wbytes=32 * 8 * 8 * 66 * 4 - 1) == WORKSPACE
+    assert size(4, 32, 8, 8, 2, 64, 4096, 0, 1, 0) == 0
+    # a window of a few tiles is never cut; the bf16 workspace does not grow with the cache
+    assert size(4, 32, 8, 8, 2, 64, 4096, 128, 0, 1) == 0
+    assert size(64, 512, 8, 64, 8, 64, 32768, 0, 0, 1) == size(64, 512, 8, 64, 8, 64, 1 << 20, 0, 0, 1)
+    # sizes that the calls refuse report none
+    assert size(4, 32, 257, 8, 2, 64, 4096, 0, 8, 1) == 0
+    assert size(4, 32, 8, 8, 2, 64, 4096, 0, 129, 1) == 0
+    assert size(4, 32, 8, 8, 2, 64, (1 << 30) + 1, 0, 8, 1) == 0 and call(Lmax=(1 << 30) + 1) == UNSUPPORTED
 
     def paged(ps=16, pages=256, num=1024, dtype=1, t=tab, Hkv=2):
         return lib.attn_sink_decode_tree_paged(q, k, v, t, cu, par, sl, s, o, l, 4, 32, 8, pages, ps, num, 8, Hkv, 64, 0,
@@ -252,6 +260,23 @@ def test_paged(page_size, window, dtype):
 def test_splits(splits, window, dtype):
     c = make_case([0, 2900, 70], [6, 30, 2], 8, 2, dtype, seed=13)
     check(c, run(c, window, 0, splits), window)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,G", [(3, 8), (7, 8), (12, 8), (40, 8)])
+@pytest.mark.parametrize("window", [0, 50])
+def test_many_short_sequences(window, T, G, dtype):
+    """More units of a tile or two than CTAs: every CTA walks several, some cut; some sequences without tokens
+    or without a cache."""
+    g = torch.Generator().manual_seed(21)
+    B = 400
+    cached = torch.randint(0, 150, (B,), generator=g).tolist()
+    ns = torch.randint(0, T + 1, (B,), generator=g).tolist()
+    cached[:5], ns[:5] = [0, 0, 600, 149, 149], [0, T, T, 0, 1]
+    c = make_case(cached, ns, 2 * G, 2, dtype, seed=22)
+    c["max_q"] = T
+    check(c, run(c, window, 16), window)
 
 
 @gpu
