@@ -48,171 +48,215 @@ struct BwdParams {
     int slabs, groups;
 };
 
-// cos and sin (times the attention factor) of pair i at position pos.  The
+// cos and sin (times the attention factor) of pair i at position pos, to out[i] and out[kPairs + i].  The
 // angle is formed in turns and reduced in fp64 (a position of 131071 leaves
 // fp32 too few bits of phase); its fraction, at most half a turn, is then
 // rounded to fp32, an error of at most 2^-24 of half a turn.
-__device__ __forceinline__ float2 rotation(const NormParams &p, int pos, int i)
+__device__ __forceinline__ void rotation(const NormParams &p, int pos, int i, float *out)
 {
     const double x = (double)pos * p.turns[i];
     float sn, cs;
     sincospif((float)(2.0 * (x - rint(x))), &sn, &cs);
-    return make_float2(cs * p.attn_factor, sn * p.attn_factor);
+    out[i] = cs * p.attn_factor;
+    out[kPairs + i] = sn * p.attn_factor;
 }
 
-// element offsets of lane l's two chunks of a head's row, and their layout in
-// registers: a[j], b[j] are the two halves of pair 8l + j
-template <bool kInter>
-__device__ __forceinline__ void unpack(const uint4 &c0, const uint4 &c1, float (&a)[8], float (&b)[8])
-{
-    const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-        if (kInter) {
-            a[j] = f.x;
-            b[j] = f.y;
-        } else if (j < 4) {
-            a[2 * j] = f.x;
-            a[2 * j + 1] = f.y;
-        } else {
-            b[2 * (j - 4)] = f.x;
-            b[2 * (j - 4) + 1] = f.y;
-        }
-    }
-}
-template <bool kInter>
-__device__ __forceinline__ void pack(const float (&a)[8], const float (&b)[8], uint4 &c0, uint4 &c1)
-{
-    uint32_t w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        w[j] = kInter ? pack_bf16x2(a[j], b[j])
-                      : (j < 4 ? pack_bf16x2(a[2 * j], a[2 * j + 1]) : pack_bf16x2(b[2 * (j - 4)], b[2 * (j - 4) + 1]));
-    c0 = make_uint4(w[0], w[1], w[2], w[3]);
-    c1 = make_uint4(w[4], w[5], w[6], w[7]);
-}
+// element offsets of lane l's two chunks of a head's row.  In registers the lane's eight pairs are two
+// arrays, a[i] the first halves of pairs 8l + 2i and 8l + 2i + 1 and b[i] their second halves, so that
+// every operation takes two pairs at a time (fp32 x 2 instructions: half the issue slots).
 template <bool kInter>
 __device__ __forceinline__ int chunk0(int l) { return kInter ? 16 * l : 8 * l; }
 template <bool kInter>
 __device__ __forceinline__ int chunk1(int l) { return kInter ? 16 * l + 8 : kPairs + 8 * l; }
 
-// lane l's 16 of a head's 64 fp32 values (bias, weight, partial sums), in pairs
-template <bool kInter>
-__device__ __forceinline__ void load_pairs(const float *p, int l, float (&a)[8], float (&b)[8])
+__device__ __forceinline__ float2 bf2(uint32_t w)
 {
-    float x[16];
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <bool kInter>
+__device__ __forceinline__ void unpack(const uint4 &c0, const uint4 &c1, float2 (&a)[4], float2 (&b)[4])
+{
+    const uint32_t w[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float4 v = reinterpret_cast<const float4 *>(p + (j < 2 ? chunk0<kInter>(l) : chunk1<kInter>(l)))[j & 1];
-        x[4 * j] = v.x;
-        x[4 * j + 1] = v.y;
-        x[4 * j + 2] = v.z;
-        x[4 * j + 3] = v.w;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        a[j] = kInter ? x[2 * j] : x[j];
-        b[j] = kInter ? x[2 * j + 1] : x[8 + j];
+    for (int i = 0; i < 4; ++i) {
+        if (kInter) {
+            a[i] = make_float2(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i + 1] << 16));
+            b[i] = make_float2(__uint_as_float(w[2 * i] & 0xffff0000u), __uint_as_float(w[2 * i + 1] & 0xffff0000u));
+        } else {
+            a[i] = bf2(w[i]);
+            b[i] = bf2(w[4 + i]);
+        }
     }
 }
 template <bool kInter>
-__device__ __forceinline__ void store_pairs(float *p, int l, const float (&a)[8], const float (&b)[8])
+__device__ __forceinline__ void pack(const float2 (&a)[4], const float2 (&b)[4], uint4 &c0, uint4 &c1)
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[kInter ? 2 * i : i] = kInter ? pack_bf16x2(a[i].x, b[i].x) : pack_bf16x2(a[i].x, a[i].y);
+        w[kInter ? 2 * i + 1 : 4 + i] = kInter ? pack_bf16x2(a[i].y, b[i].y) : pack_bf16x2(b[i].x, b[i].y);
+    }
+    c0 = make_uint4(w[0], w[1], w[2], w[3]);
+    c1 = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+// lane l's 16 of a head's 64 fp32 values (bias, weight, partial sums)
+template <bool kInter>
+__device__ __forceinline__ void load_pairs(const float *p, int l, float2 (&a)[4], float2 (&b)[4])
 {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float4 v;
-        if (kInter)
-            v = make_float4(a[2 * j], b[2 * j], a[2 * j + 1], b[2 * j + 1]);
-        else
-            v = j < 2 ? make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3])
-                      : make_float4(b[4 * j - 8], b[4 * j - 7], b[4 * j - 6], b[4 * j - 5]);
-        reinterpret_cast<float4 *>(p + (j < 2 ? chunk0<kInter>(l) : chunk1<kInter>(l)))[j & 1] = v;
+    for (int i = 0; i < 2; ++i) {
+        const float4 u = reinterpret_cast<const float4 *>(p + chunk0<kInter>(l))[i];
+        const float4 v = reinterpret_cast<const float4 *>(p + chunk1<kInter>(l))[i];
+        if (kInter) {
+            a[i] = make_float2(u.x, u.z);
+            b[i] = make_float2(u.y, u.w);
+            a[2 + i] = make_float2(v.x, v.z);
+            b[2 + i] = make_float2(v.y, v.w);
+        } else {
+            a[2 * i] = make_float2(u.x, u.y);
+            a[2 * i + 1] = make_float2(u.z, u.w);
+            b[2 * i] = make_float2(v.x, v.y);
+            b[2 * i + 1] = make_float2(v.z, v.w);
+        }
+    }
+}
+template <bool kInter>
+__device__ __forceinline__ void store_pairs(float *p, int l, const float2 (&a)[4], const float2 (&b)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        reinterpret_cast<float4 *>(p + chunk0<kInter>(l))[i] =
+            kInter ? make_float4(a[i].x, b[i].x, a[i].y, b[i].y)
+                   : make_float4(a[2 * i].x, a[2 * i].y, a[2 * i + 1].x, a[2 * i + 1].y);
+        reinterpret_cast<float4 *>(p + chunk1<kInter>(l))[i] =
+            kInter ? make_float4(a[2 + i].x, b[2 + i].x, a[2 + i].y, b[2 + i].y)
+                   : make_float4(b[2 * i].x, b[2 * i].y, b[2 * i + 1].x, b[2 * i + 1].y);
     }
 }
 
-__device__ __forceinline__ float head_sum(float x)  // over a head's 4 lanes
+// A token's rotations in shared memory: cosines, then sines of its 32 pairs.
+__device__ __forceinline__ void load_rotation(const float *rot, int l, float2 (&c)[4], float2 (&s)[4])
 {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 u = reinterpret_cast<const float4 *>(rot + 8 * l)[i];
+        const float4 v = reinterpret_cast<const float4 *>(rot + kPairs + 8 * l)[i];
+        c[2 * i] = make_float2(u.x, u.y);
+        c[2 * i + 1] = make_float2(u.z, u.w);
+        s[2 * i] = make_float2(v.x, v.y);
+        s[2 * i + 1] = make_float2(v.z, v.w);
+    }
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
+
+// sum over a head (its 4 lanes) of the products of two rows
+__device__ __forceinline__ float head_dot(const float2 (&a)[4], const float2 (&b)[4], const float2 (&c)[4],
+                                          const float2 (&d)[4])
+{
+    float2 s = fmul2(a[0], c[0]), t = fmul2(b[0], d[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        s = ffma2(a[i], c[i], s);
+        t = ffma2(b[i], d[i], t);
+    }
+    s = fadd2(s, t);
+    float x = s.x + s.y;
     x += __shfl_xor_sync(0xffffffffu, x, 1);
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
-__device__ __forceinline__ float dot16(const float (&a)[8], const float (&b)[8], const float (&c)[8],
-                                       const float (&d)[8])
-{
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s = fmaf(a[j], c[j], fmaf(b[j], d[j], s));
-    return s;
-}
 
 // ------------------------------------------------------------------ forward
-// kTok tokens per CTA: their rotations into shared memory (one angle a
-// thread), then 64 heads at a time.
-constexpr int kTok = 8;
+// A CTA takes TOK tokens, 64 heads at a time, a thread kUnits heads' chunks at a time with
+// all of their loads issued first (the first ones before the rotations are formed, one angle a
+// thread, in shared memory).
+constexpr int kUnits = 4;
 
-template <bool kInter>
+template <bool kInter, int TOK>
 __global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(const NormParams p, __nv_bfloat16 *__restrict__ q,
                                                                __nv_bfloat16 *__restrict__ k,
                                                                __nv_bfloat16 *__restrict__ v)
 {
-    __shared__ float2 rot[kTok][kPairs];
-    const int t0 = blockIdx.x * kTok;
-    for (int a = threadIdx.x; a < kTok * kPairs; a += kThreads)
-        if (t0 + a / kPairs < p.T) rot[a / kPairs][a % kPairs] = rotation(p, p.pos[t0 + a / kPairs], a % kPairs);
-    __syncthreads();
+    __shared__ __align__(16) float rot[TOK][2 * kPairs];
+    const int t0 = blockIdx.x * TOK;
     const int heads = p.Hq + 2 * p.Hkv, l = threadIdx.x & 3;
-    const int units = min(kTok, p.T - t0) * heads;
-    for (int base = 0; base < units; base += kThreads / 4) {  // uniform: the shuffles need whole warps
-        const int u = base + (threadIdx.x >> 2);
-        const bool live = u < units;
-        const int tt = live ? u / heads : 0, h = live ? u % heads : 0, t = t0 + tt;
-        const int kr = p.kv_rows && h >= p.Hq ? p.kv_rows[t] : t;
-        const __nv_bfloat16 *src = p.qkv + ((size_t)t * heads + h) * kD;
-        float a[8], b[8];
-        unpack<kInter>(*reinterpret_cast<const uint4 *>(src + chunk0<kInter>(l)),
-                       *reinterpret_cast<const uint4 *>(src + chunk1<kInter>(l)), a, b);
-        if (p.bias) {
-            float ba[8], bb[8];
-            load_pairs<kInter>(p.bias + h * kD, l, ba, bb);
+    const int units = min(TOK, p.T - t0) * heads;
+    const __nv_bfloat16 *src0 = p.qkv + (size_t)t0 * heads * kD;  // units are consecutive rows of kD values
+    constexpr int kStep = kThreads / 4;
+    uint4 c0[kUnits], c1[kUnits];
+    auto load = [&](int base) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a[j] += ba[j];
-                b[j] += bb[j];
-            }
+        for (int i = 0; i < kUnits; ++i) {
+            const int u = base + i * kStep;
+            const __nv_bfloat16 *src = src0 + (size_t)(u < units ? u : 0) * kD;
+            c0[i] = *reinterpret_cast<const uint4 *>(src + chunk0<kInter>(l));
+            c1[i] = *reinterpret_cast<const uint4 *>(src + chunk1<kInter>(l));
         }
-        const float r = rsqrtf(head_sum(dot16(a, b, a, b)) * (1.f / kD) + p.eps);
-        if (h < p.Hq + p.Hkv) {
-            float wa[8], wb[8];
-            load_pairs<kInter>(h < p.Hq ? p.qw : p.kw, l, wa, wb);
+    };
+    load(threadIdx.x >> 2);
+    for (int a = threadIdx.x; a < TOK * kPairs; a += kThreads)
+        if (t0 + a / kPairs < p.T) rotation(p, p.pos[t0 + a / kPairs], a % kPairs, rot[a / kPairs]);
+    __syncthreads();
+    for (int base = threadIdx.x >> 2;; base += kUnits * kStep) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 cs = rot[tt][8 * l + j];
-                const float x = a[j] * r * wa[j], y = b[j] * r * wb[j];
-                a[j] = x * cs.x - y * cs.y;
-                b[j] = y * cs.x + x * cs.y;
+        for (int i = 0; i < kUnits; ++i) {  // (the shuffles need whole warps: no lane leaves)
+            const int u = base + i * kStep;
+            const bool live = u < units;
+            const int tt = live ? u / heads : 0, h = live ? u % heads : 0, t = t0 + tt;
+            const int kr = p.kv_rows && h >= p.Hq ? p.kv_rows[t] : t;
+            float2 a[4], b[4];
+            unpack<kInter>(c0[i], c1[i], a, b);
+            if (p.bias) {
+                float2 ba[4], bb[4];
+                load_pairs<kInter>(p.bias + h * kD, l, ba, bb);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a[j] = fadd2(a[j], ba[j]);
+                    b[j] = fadd2(b[j], bb[j]);
+                }
             }
+            const float r = rsqrtf(head_dot(a, b, a, b) * (1.f / kD) + p.eps);
+            if (h < p.Hq + p.Hkv) {
+                float2 wa[4], wb[4], c[4], s[4];
+                load_pairs<kInter>(h < p.Hq ? p.qw : p.kw, l, wa, wb);
+                load_rotation(rot[tt], l, c, s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = fmul2(fmul2(a[j], both(r)), wa[j]), y = fmul2(fmul2(b[j], both(r)), wb[j]);
+                    a[j] = ffma2(x, c[j], neg2(fmul2(y, s[j])));
+                    b[j] = ffma2(y, c[j], fmul2(x, s[j]));
+                }
+            }
+            if (!live || (h >= p.Hq && (kr < 0 || kr >= p.kv_rows_total))) continue;
+            __nv_bfloat16 *dst = h < p.Hq              ? q + ((size_t)t * p.Hq + h) * kD
+                                 : h < p.Hq + p.Hkv ? k + ((size_t)kr * p.Hkv + (h - p.Hq)) * kD
+                                                    : v + ((size_t)kr * p.Hkv + (h - p.Hq - p.Hkv)) * kD;
+            uint4 o0, o1;
+            pack<kInter>(a, b, o0, o1);
+            *reinterpret_cast<uint4 *>(dst + chunk0<kInter>(l)) = o0;
+            *reinterpret_cast<uint4 *>(dst + chunk1<kInter>(l)) = o1;
         }
-        if (!live || (h >= p.Hq && (kr < 0 || kr >= p.kv_rows_total))) continue;
-        __nv_bfloat16 *dst = h < p.Hq              ? q + ((size_t)t * p.Hq + h) * kD
-                             : h < p.Hq + p.Hkv ? k + ((size_t)kr * p.Hkv + (h - p.Hq)) * kD
-                                                : v + ((size_t)kr * p.Hkv + (h - p.Hq - p.Hkv)) * kD;
-        uint4 c0, c1;
-        pack<kInter>(a, b, c0, c1);
-        *reinterpret_cast<uint4 *>(dst + chunk0<kInter>(l)) = c0;
-        *reinterpret_cast<uint4 *>(dst + chunk1<kInter>(l)) = c1;
+        if (base - (int)(threadIdx.x >> 2) + kUnits * kStep >= units) break;  // uniform over the CTA
+        load(base + kUnits * kStep);
     }
 }
 
 // ------------------------------------------------------------------ backward
 // CTA = (16 heads, slab of tokens): 4 tokens x 16 heads x 4 lanes at a time, so
 // a thread keeps its head and its 16 columns, whose dbias and weight sums stay
-// in its registers over the slab.  The four token lanes then add up through
-// shared memory and the CTA stores one partial row; a second kernel sums the
-// slabs in order, so the gradients are the same from run to run.
+// in its registers over the slab.  The rows come through a ring in shared memory of kRing
+// steps, each thread copying (asynchronously) the 64 bytes it will read itself,
+// so that no barrier and no register holds a load in flight.  The four token lanes
+// then add up through shared memory and the CTA stores one partial row; a
+// second kernel sums the slabs in order, so the gradients are the same from run to run.
 constexpr int kHeads = 16;
 constexpr int kTokLanes = kThreads / (4 * kHeads);
-constexpr int kBTok = 8;           // tokens whose rotations are formed at a time
+constexpr int kBTok = 16;          // tokens whose rotations are formed at a time
+constexpr int kRing = 5;
 constexpr int kMaxSlabs = 256;
+constexpr int kBwdSmem = kRing * 4 * kThreads * 16;
 
 __host__ __device__ __forceinline__ int head_groups(int heads) { return (heads + kHeads - 1) / kHeads; }
 __host__ __forceinline__ int num_slabs(int T)
@@ -221,13 +265,20 @@ __host__ __forceinline__ int num_slabs(int T)
     return s < kMaxSlabs ? s : kMaxSlabs;
 }
 
+__device__ __forceinline__ void copy16_async(uint32_t smem_dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
+}
+
 template <bool kInter>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const BwdParams bp)
+__global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const BwdParams bp)
 {
     grid_dep_launch();
     const NormParams &p = bp.n;
-    __shared__ float2 rot[kBTok][kPairs];
-    __shared__ float red[kTokLanes][kHeads * kD];
+    __shared__ __align__(16) float rot[2][kBTok][2 * kPairs];
+    extern __shared__ __align__(16) uint8_t ring_raw[];  // [kRing][4 chunks][kThreads] of 16 bytes
+    static_assert(kTokLanes * kHeads * kD * 4 <= kBwdSmem, "the sums' exchange reuses the ring");
+    float *red = reinterpret_cast<float *>(ring_raw);  // [kTokLanes][kHeads * kD]
     const int heads = p.Hq + 2 * p.Hkv;
     const int group = blockIdx.x % bp.groups, slab = blockIdx.x / bp.groups;
     const int l = threadIdx.x & 3, hs = (threadIdx.x >> 2) % kHeads, tl = threadIdx.x / (4 * kHeads);
@@ -235,84 +286,110 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const BwdParams b
     const bool is_q = h < p.Hq, rotated = h < p.Hq + p.Hkv, live_h = h < heads;
     const int hc = live_h ? h : 0;
     const long long tb = (long long)p.T * slab / bp.slabs, te = (long long)p.T * (slab + 1) / bp.slabs;
-    float ba[8], bb[8], wa[8], wb[8], sa[8], sb[8], ga[8], gb[8];  // bias, weight, dbias sums, weight sums
+    const int nt = (int)(te - tb);  // tokens of the slab
+    // this thread's rows: token tb + tl of the inputs and of the gradient of its head, and their strides
+    const __nv_bfloat16 *src = p.qkv + ((size_t)tb * heads + hc) * kD;
+    const size_t gs = is_q || !live_h ? (size_t)p.Hq * kD : (size_t)p.Hkv * kD, ss = (size_t)heads * kD;
+    const __nv_bfloat16 *gsrc = (is_q || !live_h ? bp.dq + (live_h ? h : 0) * kD
+                                 : rotated       ? bp.dk + (h - p.Hq) * kD
+                                                 : bp.dv + (h - p.Hq - p.Hkv) * kD) + tb * gs;
+    const uint32_t ring = smem_u32(ring_raw) + threadIdx.x * 16;
+    auto fetch = [&](int step) {  // the step-th token of this lane
+        const int t = step * kTokLanes + tl;
+        if (t < nt) {
+            const uint32_t dst = ring + (step % kRing) * 4 * kThreads * 16;
+            copy16_async(dst, src + t * ss + chunk0<kInter>(l));
+            copy16_async(dst + kThreads * 16, src + t * ss + chunk1<kInter>(l));
+            copy16_async(dst + 2 * kThreads * 16, gsrc + t * gs + chunk0<kInter>(l));
+            copy16_async(dst + 3 * kThreads * 16, gsrc + t * gs + chunk1<kInter>(l));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto rotations = [&](int t0) {  // of tokens [t0, t0 + kBTok) of the slab
+        for (int a = threadIdx.x; a < kBTok * kPairs; a += kThreads)
+            if (t0 + a / kPairs < nt)
+                rotation(p, p.pos[tb + t0 + a / kPairs], a % kPairs, rot[t0 / kBTok & 1][a / kPairs]);
+    };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ba[j] = bb[j] = sa[j] = sb[j] = ga[j] = gb[j] = 0.f;
+    for (int s = 0; s < kRing - 1; ++s) fetch(s);
+    float2 ba[4], bb[4], wa[4], wb[4], sa[4], sb[4], ga[4], gb[4];  // bias, weight, dbias sums, weight sums
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ba[j] = bb[j] = sa[j] = sb[j] = ga[j] = gb[j] = make_float2(0.f, 0.f);
     if (p.bias) load_pairs<kInter>(p.bias + hc * kD, l, ba, bb);
     load_pairs<kInter>(is_q ? p.qw : p.kw, l, wa, wb);
-    for (long long t0 = tb; t0 < te; t0 += kBTok) {
-        __syncthreads();
-        for (int a = threadIdx.x; a < kBTok * kPairs; a += kThreads)
-            if (t0 + a / kPairs < te) rot[a / kPairs][a % kPairs] = rotation(p, p.pos[t0 + a / kPairs], a % kPairs);
-        __syncthreads();
-        for (int tt = tl; tt < kBTok; tt += kTokLanes) {
-            const bool live = live_h && t0 + tt < te;
-            const size_t t = live ? t0 + tt : tb;
-            const __nv_bfloat16 *src = p.qkv + (t * heads + hc) * kD;
-            const __nv_bfloat16 *gsrc = is_q || !live_h ? bp.dq + (t * p.Hq + (live_h ? h : 0)) * kD
-                                        : rotated     ? bp.dk + (t * p.Hkv + (h - p.Hq)) * kD
-                                                      : bp.dv + (t * p.Hkv + (h - p.Hq - p.Hkv)) * kD;
-            float a[8], b[8], ua[8], ub[8];
-            unpack<kInter>(*reinterpret_cast<const uint4 *>(src + chunk0<kInter>(l)),
-                           *reinterpret_cast<const uint4 *>(src + chunk1<kInter>(l)), a, b);
-            unpack<kInter>(*reinterpret_cast<const uint4 *>(gsrc + chunk0<kInter>(l)),
-                           *reinterpret_cast<const uint4 *>(gsrc + chunk1<kInter>(l)), ua, ub);
+    rotations(0);
+    int step = 0;
+    for (int t0 = 0; t0 < nt; t0 += kBTok) {
+        __syncthreads();  // this batch's rotations are there, and the other buffer's readers done
+        if (t0 + kBTok < nt) rotations(t0 + kBTok);
+#pragma unroll 1
+        for (int tt = tl; tt < kBTok; tt += kTokLanes, ++step) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            const bool live = live_h && t0 + tt < nt;
+            const uint4 *mine = reinterpret_cast<const uint4 *>(ring_raw) + (step % kRing) * 4 * kThreads + threadIdx.x;
+            float2 a[4], b[4], ua[4], ub[4];
+            unpack<kInter>(mine[0], mine[kThreads], a, b);
+            unpack<kInter>(mine[2 * kThreads], mine[3 * kThreads], ua, ub);
+            fetch(step + kRing - 1);  // into the step before's place
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                a[j] += ba[j];
-                b[j] += bb[j];
+            for (int j = 0; j < 4; ++j) {
+                a[j] = fadd2(a[j], ba[j]);
+                b[j] = fadd2(b[j], bb[j]);
             }
-            const float r = rsqrtf(head_sum(dot16(a, b, a, b)) * (1.f / kD) + p.eps);
+            const float r = rsqrtf(head_dot(a, b, a, b) * (1.f / kD) + p.eps);
             if (rotated) {
+                float2 c[4], s[4];
+                load_rotation(rot[t0 / kBTok & 1][tt], l, c, s);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 cs = rot[tt][8 * l + j];
-                    const float x = ua[j] * cs.x + ub[j] * cs.y, y = ub[j] * cs.x - ua[j] * cs.y;
-                    a[j] *= r;  // n
-                    b[j] *= r;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = ffma2(ua[j], c[j], fmul2(ub[j], s[j]));
+                    const float2 y = ffma2(ub[j], c[j], neg2(fmul2(ua[j], s[j])));
+                    a[j] = fmul2(a[j], both(r));  // n
+                    b[j] = fmul2(b[j], both(r));
                     if (live) {
-                        ga[j] = fmaf(x, a[j], ga[j]);
-                        gb[j] = fmaf(y, b[j], gb[j]);
+                        ga[j] = ffma2(x, a[j], ga[j]);
+                        gb[j] = ffma2(y, b[j], gb[j]);
                     }
-                    ua[j] = x * wa[j];
-                    ub[j] = y * wb[j];
+                    ua[j] = fmul2(x, wa[j]);
+                    ub[j] = fmul2(y, wb[j]);
                 }
             }
-            const float mean = head_sum(dot16(ua, ub, a, b)) * (1.f / kD);
+            const float2 mean = both(-head_dot(ua, ub, a, b) * (1.f / kD));
             if (rotated) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    ua[j] = r * fmaf(-mean, a[j], ua[j]);
-                    ub[j] = r * fmaf(-mean, b[j], ub[j]);
+                for (int j = 0; j < 4; ++j) {
+                    ua[j] = fmul2(both(r), ffma2(mean, a[j], ua[j]));
+                    ub[j] = fmul2(both(r), ffma2(mean, b[j], ub[j]));
                 }
             }
             if (live) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sa[j] += ua[j];
-                    sb[j] += ub[j];
+                for (int j = 0; j < 4; ++j) {
+                    sa[j] = fadd2(sa[j], ua[j]);
+                    sb[j] = fadd2(sb[j], ub[j]);
                 }
                 uint4 c0, c1;
                 pack<kInter>(ua, ub, c0, c1);
-                __nv_bfloat16 *dst = bp.dqkv + (t * heads + h) * kD;
+                __nv_bfloat16 *dst = bp.dqkv + ((size_t)(tb + t0 + tt) * heads + h) * kD;
                 *reinterpret_cast<uint4 *>(dst + chunk0<kInter>(l)) = c0;
                 *reinterpret_cast<uint4 *>(dst + chunk1<kInter>(l)) = c1;
             }
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     // partial rows: [slab][groups * kHeads * D] dbias, then [slab][groups][2][D] weights
     const size_t wide = (size_t)bp.groups * kHeads * kD;
     __syncthreads();
-    store_pairs<kInter>(&red[tl][hs * kD], l, sa, sb);
+    store_pairs<kInter>(red + (tl * kHeads + hs) * kD, l, sa, sb);
     __syncthreads();
     for (int c = threadIdx.x; c < kHeads * kD; c += kThreads) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kTokLanes; ++w) s += red[w][c];
+        for (int w = 0; w < kTokLanes; ++w) s += red[w * kHeads * kD + c];
         bp.ws[slab * wide + (size_t)group * kHeads * kD + c] = s;
     }
     __syncthreads();
-    store_pairs<kInter>(&red[tl][hs * kD], l, ga, gb);
+    store_pairs<kInter>(red + (tl * kHeads + hs) * kD, l, ga, gb);
     __syncthreads();
     if (threadIdx.x < 2 * kD) {
         const int which = threadIdx.x / kD, d = threadIdx.x % kD;  // 0: q, 1: k
@@ -321,7 +398,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const BwdParams b
             const int hh = group * kHeads + x;
             if (which == 0 ? hh < p.Hq : hh >= p.Hq && hh < p.Hq + p.Hkv)
 #pragma unroll
-                for (int w = 0; w < kTokLanes; ++w) s += red[w][x * kD + d];
+                for (int w = 0; w < kTokLanes; ++w) s += red[(w * kHeads + x) * kD + d];
         }
         bp.ws[bp.slabs * wide + (((size_t)slab * bp.groups + group) * 2 + which) * kD + d] = s;
     }
@@ -384,10 +461,13 @@ cudaError_t launch_qk_norm_prologue(const void *qkv, const float *bias, const Qk
                                     int kv_rows_total, const RopeParams &r, cudaStream_t st)
 {
     const NormParams p = norm_params(qkv, bias, n, positions, kv_rows, T, Hq, Hkv, kv_rows_total, r);
-    auto kern = r.interleaved ? qk_norm_fwd_kernel<true> : qk_norm_fwd_kernel<false>;
-    kern<<<(T + kTok - 1) / kTok, kThreads, 0, st>>>(p, static_cast<__nv_bfloat16 *>(q),
-                                                     static_cast<__nv_bfloat16 *>(k),
-                                                     static_cast<__nv_bfloat16 *>(v));
+    // two tokens a CTA while that leaves no more CTAs than run at once, else eight
+    const bool few = T <= 2 * 4 * 148;
+    const int tok = few ? 2 : 8;
+    auto kern = few ? (r.interleaved ? qk_norm_fwd_kernel<true, 2> : qk_norm_fwd_kernel<false, 2>)
+                    : (r.interleaved ? qk_norm_fwd_kernel<true, 8> : qk_norm_fwd_kernel<false, 8>);
+    kern<<<(T + tok - 1) / tok, kThreads, 0, st>>>(p, static_cast<__nv_bfloat16 *>(q), static_cast<__nv_bfloat16 *>(k),
+                                                   static_cast<__nv_bfloat16 *>(v));
     return cudaGetLastError();
 }
 
@@ -415,8 +495,10 @@ cudaError_t launch_qk_norm_bwd(const void *qkv, const float *bias, const QkNorm 
     p.slabs = num_slabs(T);
     p.groups = head_groups(Hq + 2 * Hkv);
     auto kern = r.interleaved ? qk_norm_bwd_kernel<true> : qk_norm_bwd_kernel<false>;
-    kern<<<p.slabs * p.groups, kThreads, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    if (e != cudaSuccess) return e;
+    kern<<<p.slabs * p.groups, kThreads, kBwdSmem, st>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((dbias ? Hq + 2 * Hkv : 0) + 2));

@@ -631,6 +631,15 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b)
     return d;
 }
 
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(*reinterpret_cast<unsigned long long *>(&d))
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)));
+    return d;
+}
+
 __device__ __forceinline__ float2 fsub2(float2 a, float2 b)
 {
     float2 d;
