@@ -168,101 +168,20 @@ __device__ __forceinline__ float head_dot(const float2 (&a)[4], const float2 (&b
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-// ------------------------------------------------------------------ forward
-// A CTA takes TOK tokens, 64 heads at a time, a thread kUnits heads' chunks at a time with
-// all of their loads issued first (the first ones before the rotations are formed, one angle a
-// thread, in shared memory).
-constexpr int kUnits = 4;
-
-template <bool kInter, int TOK>
-__global__ void __launch_bounds__(kThreads) qk_norm_fwd_kernel(const NormParams p, __nv_bfloat16 *__restrict__ q,
-                                                               __nv_bfloat16 *__restrict__ k,
-                                                               __nv_bfloat16 *__restrict__ v)
-{
-    __shared__ __align__(16) float rot[TOK][2 * kPairs];
-    const int t0 = blockIdx.x * TOK;
-    const int heads = p.Hq + 2 * p.Hkv, l = threadIdx.x & 3;
-    const int units = min(TOK, p.T - t0) * heads;
-    const __nv_bfloat16 *src0 = p.qkv + (size_t)t0 * heads * kD;  // units are consecutive rows of kD values
-    constexpr int kStep = kThreads / 4;
-    uint4 c0[kUnits], c1[kUnits];
-    auto load = [&](int base) {
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {
-            const int u = base + i * kStep;
-            const __nv_bfloat16 *src = src0 + (size_t)(u < units ? u : 0) * kD;
-            c0[i] = *reinterpret_cast<const uint4 *>(src + chunk0<kInter>(l));
-            c1[i] = *reinterpret_cast<const uint4 *>(src + chunk1<kInter>(l));
-        }
-    };
-    load(threadIdx.x >> 2);
-    for (int a = threadIdx.x; a < TOK * kPairs; a += kThreads)
-        if (t0 + a / kPairs < p.T) rotation(p, p.pos[t0 + a / kPairs], a % kPairs, rot[a / kPairs]);
-    __syncthreads();
-    for (int base = threadIdx.x >> 2;; base += kUnits * kStep) {
-#pragma unroll
-        for (int i = 0; i < kUnits; ++i) {  // (the shuffles need whole warps: no lane leaves)
-            const int u = base + i * kStep;
-            const bool live = u < units;
-            const int tt = live ? u / heads : 0, h = live ? u % heads : 0, t = t0 + tt;
-            const int kr = p.kv_rows && h >= p.Hq ? p.kv_rows[t] : t;
-            float2 a[4], b[4];
-            unpack<kInter>(c0[i], c1[i], a, b);
-            if (p.bias) {
-                float2 ba[4], bb[4];
-                load_pairs<kInter>(p.bias + h * kD, l, ba, bb);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    a[j] = fadd2(a[j], ba[j]);
-                    b[j] = fadd2(b[j], bb[j]);
-                }
-            }
-            const float r = rsqrtf(head_dot(a, b, a, b) * (1.f / kD) + p.eps);
-            if (h < p.Hq + p.Hkv) {
-                float2 wa[4], wb[4], c[4], s[4];
-                load_pairs<kInter>(h < p.Hq ? p.qw : p.kw, l, wa, wb);
-                load_rotation(rot[tt], l, c, s);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 x = fmul2(fmul2(a[j], both(r)), wa[j]), y = fmul2(fmul2(b[j], both(r)), wb[j]);
-                    a[j] = ffma2(x, c[j], neg2(fmul2(y, s[j])));
-                    b[j] = ffma2(y, c[j], fmul2(x, s[j]));
-                }
-            }
-            if (!live || (h >= p.Hq && (kr < 0 || kr >= p.kv_rows_total))) continue;
-            __nv_bfloat16 *dst = h < p.Hq              ? q + ((size_t)t * p.Hq + h) * kD
-                                 : h < p.Hq + p.Hkv ? k + ((size_t)kr * p.Hkv + (h - p.Hq)) * kD
-                                                    : v + ((size_t)kr * p.Hkv + (h - p.Hq - p.Hkv)) * kD;
-            uint4 o0, o1;
-            pack<kInter>(a, b, o0, o1);
-            *reinterpret_cast<uint4 *>(dst + chunk0<kInter>(l)) = o0;
-            *reinterpret_cast<uint4 *>(dst + chunk1<kInter>(l)) = o1;
-        }
-        if (base - (int)(threadIdx.x >> 2) + kUnits * kStep >= units) break;  // uniform over the CTA
-        load(base + kUnits * kStep);
-    }
-}
-
-// ------------------------------------------------------------------ backward
-// CTA = (16 heads, slab of tokens): 4 tokens x 16 heads x 4 lanes at a time, so
-// a thread keeps its head and its 16 columns, whose dbias and weight sums stay
-// in its registers over the slab.  The rows come through a ring in shared memory of kRing
-// steps, each thread copying (asynchronously) the 64 bytes it will read itself,
-// so that no barrier and no register holds a load in flight.  The four token lanes
-// then add up through shared memory and the CTA stores one partial row; a
-// second kernel sums the slabs in order, so the gradients are the same from run to run.
+// Both kernels: CTA = (16 heads, a slab of tokens), 4 tokens x 16 heads x 4 lanes a step, so a thread keeps
+// its head, and with it the bias and the weights of its 16 columns, in registers.  The slabs are as many as
+// run at once.  The rows come through a ring in shared memory, each thread copying (asynchronously)
+// the bytes it will read itself, so that no barrier and no register holds a load in flight.  The rotations
+// of kBTok tokens at a time are formed in shared memory, one angle a thread, a batch ahead.
 constexpr int kHeads = 16;
 constexpr int kTokLanes = kThreads / (4 * kHeads);
-constexpr int kBTok = 16;          // tokens whose rotations are formed at a time
-constexpr int kRing = 5;
-constexpr int kMaxSlabs = 256;
-constexpr int kBwdSmem = kRing * 4 * kThreads * 16;
-
+constexpr int kBTok = 16;
 __host__ __device__ __forceinline__ int head_groups(int heads) { return (heads + kHeads - 1) / kHeads; }
-__host__ __forceinline__ int num_slabs(int T)
+// slabs of T tokens for `ctas` CTAs in all; at least a step's tokens each
+__host__ __forceinline__ int num_slabs(int T, int groups, int ctas)
 {
-    const int s = (T + kBTok - 1) / kBTok;
-    return s < kMaxSlabs ? s : kMaxSlabs;
+    const int most = (T + kTokLanes - 1) / kTokLanes, fit = ctas / groups > 0 ? ctas / groups : 1;
+    return most < fit ? most : fit;
 }
 
 __device__ __forceinline__ void copy16_async(uint32_t smem_dst, const void *src)
@@ -270,8 +189,107 @@ __device__ __forceinline__ void copy16_async(uint32_t smem_dst, const void *src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
 }
 
+// ------------------------------------------------------------------ forward
+constexpr int kFwdRing = 4, kFwdPerSm = 3;
+
 template <bool kInter>
-__global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const BwdParams bp)
+__global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const NormParams p, int slabs,
+                                                                          __nv_bfloat16 *__restrict__ q,
+                                                                          __nv_bfloat16 *__restrict__ k,
+                                                                          __nv_bfloat16 *__restrict__ v)
+{
+    __shared__ __align__(16) float rot[2][kBTok][2 * kPairs];
+    extern __shared__ __align__(16) uint8_t ring_raw[];  // [kFwdRing][2 chunks][kThreads] of 16 bytes
+    const int heads = p.Hq + 2 * p.Hkv, groups = head_groups(heads);
+    const int slab = blockIdx.x / groups;
+    const int l = threadIdx.x & 3, h = blockIdx.x % groups * kHeads + (threadIdx.x >> 2) % kHeads;
+    const int tl = threadIdx.x / (4 * kHeads);
+    const bool live_h = h < heads;
+    const int hc = live_h ? h : 0;
+    const long long tb = (long long)p.T * slab / slabs;
+    const int nt = (int)((long long)p.T * (slab + 1) / slabs - tb);  // tokens of the slab
+    const size_t ss = (size_t)heads * kD;
+    const __nv_bfloat16 *src = p.qkv + tb * ss + hc * kD;
+    const uint32_t ring = smem_u32(ring_raw) + threadIdx.x * 16;
+    auto fetch = [&](int step) {  // the step-th token of this lane
+        const int t = step * kTokLanes + tl;
+        if (t < nt) {
+            const uint32_t dst = ring + (step % kFwdRing) * 2 * kThreads * 16;
+            copy16_async(dst, src + t * ss + chunk0<kInter>(l));
+            copy16_async(dst + kThreads * 16, src + t * ss + chunk1<kInter>(l));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto rotations = [&](int t0) {  // of tokens [t0, t0 + kBTok) of the slab
+        for (int a = threadIdx.x; a < kBTok * kPairs; a += kThreads)
+            if (t0 + a / kPairs < nt)
+                rotation(p, p.pos[tb + t0 + a / kPairs], a % kPairs, rot[t0 / kBTok & 1][a / kPairs]);
+    };
+#pragma unroll
+    for (int s = 0; s < kFwdRing - 1; ++s) fetch(s);
+    float2 ba[4], bb[4], wa[4], wb[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ba[j] = bb[j] = make_float2(0.f, 0.f);
+    if (p.bias) load_pairs<kInter>(p.bias + hc * kD, l, ba, bb);
+    load_pairs<kInter>(h < p.Hq ? p.qw : p.kw, l, wa, wb);
+    rotations(0);
+    // where its rows go: q by token, k and v by cache row
+    const bool is_q = h < p.Hq;
+    __nv_bfloat16 *out = is_q ? q + h * kD : h < p.Hq + p.Hkv ? k + (h - p.Hq) * kD : v + (h - p.Hq - p.Hkv) * kD;
+    const size_t stride = (size_t)(is_q ? p.Hq : p.Hkv) * kD;
+    int step = 0;
+    for (int t0 = 0; t0 < nt; t0 += kBTok) {
+        __syncthreads();  // this batch's rotations are there, and the other buffer's readers done
+        if (t0 + kBTok < nt) rotations(t0 + kBTok);
+        const int n = min(kBTok, nt - t0);
+#pragma unroll 1
+        for (int x = 0; x < n; x += kTokLanes, ++step) {  // (the shuffles need whole warps: no lane leaves)
+            const int tt = x + tl;
+            const bool live = live_h && tt < n;
+            const long long t = tb + t0 + tt;
+            const long long row = !is_q && p.kv_rows && live ? p.kv_rows[t] : t;
+            asm volatile("cp.async.wait_group %0;" ::"n"(kFwdRing - 2) : "memory");
+            const uint4 *mine = reinterpret_cast<const uint4 *>(ring_raw) + (step % kFwdRing) * 2 * kThreads + threadIdx.x;
+            float2 a[4], b[4];
+            unpack<kInter>(mine[0], mine[kThreads], a, b);
+            fetch(step + kFwdRing - 1);  // into the step before's place
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a[j] = fadd2(a[j], ba[j]);
+                b[j] = fadd2(b[j], bb[j]);
+            }
+            const float r = rsqrtf(head_dot(a, b, a, b) * (1.f / kD) + p.eps);
+            if (h < p.Hq + p.Hkv) {
+                float2 c[4], s[4];
+                load_rotation(rot[t0 / kBTok & 1][tt], l, c, s);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 x = fmul2(fmul2(a[j], both(r)), wa[j]), y = fmul2(fmul2(b[j], both(r)), wb[j]);
+                    a[j] = ffma2(x, c[j], neg2(fmul2(y, s[j])));
+                    b[j] = ffma2(y, c[j], fmul2(x, s[j]));
+                }
+            }
+            if (live && (is_q || (row >= 0 && row < p.kv_rows_total))) {
+                __nv_bfloat16 *dst = out + row * stride;
+                uint4 o0, o1;
+                pack<kInter>(a, b, o0, o1);
+                *reinterpret_cast<uint4 *>(dst + chunk0<kInter>(l)) = o0;
+                *reinterpret_cast<uint4 *>(dst + chunk1<kInter>(l)) = o1;
+            }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ------------------------------------------------------------------ backward
+// A thread's dbias and weight sums stay in its registers over its slab.  The four token lanes then add up
+// through shared memory and the CTA stores one partial row; a second kernel sums the slabs in order, so the
+// gradients are the same from run to run.
+constexpr int kRing = 3, kBwdPerSm = 2;
+constexpr int kBwdSmem = kRing * 4 * kThreads * 16;
+
+template <bool kInter>
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) qk_norm_bwd_kernel(const BwdParams bp)
 {
     grid_dep_launch();
     const NormParams &p = bp.n;
@@ -323,8 +341,9 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const BwdParam
         __syncthreads();  // this batch's rotations are there, and the other buffer's readers done
         if (t0 + kBTok < nt) rotations(t0 + kBTok);
 #pragma unroll 1
-        for (int tt = tl; tt < kBTok; tt += kTokLanes, ++step) {
+        for (int x = 0; x < min(kBTok, nt - t0); x += kTokLanes, ++step) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            const int tt = x + tl;
             const bool live = live_h && t0 + tt < nt;
             const uint4 *mine = reinterpret_cast<const uint4 *>(ring_raw) + (step % kRing) * 4 * kThreads + threadIdx.x;
             float2 a[4], b[4], ua[4], ub[4];
@@ -404,34 +423,38 @@ __global__ void __launch_bounds__(kThreads, 2) qk_norm_bwd_kernel(const BwdParam
     }
 }
 
-// column sums over the slabs, in order; the last two CTAs take the weights
+// Column sums over the slabs, in order: a CTA takes 64 columns, 16 threads of four columns for each of 16
+// parts of the slabs; the last two CTAs take the weights.
 __global__ void __launch_bounds__(kThreads) qk_norm_finish_kernel(const BwdParams bp)
 {
-    grid_dep_wait();
-    const int heads = bp.n.Hq + 2 * bp.n.Hkv;
+    constexpr int kParts = kThreads / (kD / 4);
+    __shared__ __align__(16) float red[kParts][kD];
     const size_t wide = (size_t)bp.groups * kHeads * kD;
-    __shared__ float red[kThreads];
-    const int bias_ctas = gridDim.x - 2;
-    const int col = threadIdx.x % kD, part = threadIdx.x / kD;
-    constexpr int kParts = kThreads / kD;
-    float s = 0.f;
-    if ((int)blockIdx.x < bias_ctas) {
-        for (int x = part; x < bp.slabs; x += kParts) s += bp.ws[x * wide + (size_t)blockIdx.x * kD + col];
-    } else {
-        const int which = blockIdx.x - bias_ctas;
-        const float *w = bp.ws + bp.slabs * wide;
-        for (int x = part; x < bp.slabs * bp.groups; x += kParts) s += w[((size_t)x * 2 + which) * kD + col];
+    const int bias_ctas = gridDim.x - 2, which = (int)blockIdx.x - bias_ctas;  // which >= 0: q's, k's weights
+    const int col = threadIdx.x % (kD / 4) * 4, part = threadIdx.x / (kD / 4);
+    const float *src = which < 0 ? bp.ws + (size_t)blockIdx.x * kD : bp.ws + bp.slabs * wide + which * kD;
+    const size_t stride = which < 0 ? wide : 2 * kD;
+    const int n = which < 0 ? bp.slabs : bp.slabs * bp.groups;
+    grid_dep_wait();
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int x = part; x < n; x += kParts) {
+        const float4 v = *reinterpret_cast<const float4 *>(src + x * stride + col);
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
     }
-    red[threadIdx.x] = s;
+    *reinterpret_cast<float4 *>(&red[part][col]) = s;
     __syncthreads();
-    if (part != 0) return;
+    if (threadIdx.x >= kD) return;
+    float t = 0.f;
 #pragma unroll
-    for (int w = 1; w < kParts; ++w) s += red[w * kD + col];
-    if ((int)blockIdx.x < bias_ctas) {
-        if ((int)blockIdx.x < heads) bp.dbias[(size_t)blockIdx.x * kD + col] = s;
-    } else {
-        (blockIdx.x == (unsigned)bias_ctas ? bp.dqw : bp.dkw)[col] = s;
-    }
+    for (int w = 0; w < kParts; ++w) t += red[w][threadIdx.x];
+    if (which < 0)
+        bp.dbias[(size_t)blockIdx.x * kD + threadIdx.x] = t;
+    else
+        (which == 0 ? bp.dqw : bp.dkw)[threadIdx.x] = t;
 }
 
 NormParams norm_params(const void *qkv, const float *bias, const QkNorm &n, const int *positions, const int *kv_rows,
@@ -461,20 +484,21 @@ cudaError_t launch_qk_norm_prologue(const void *qkv, const float *bias, const Qk
                                     int kv_rows_total, const RopeParams &r, cudaStream_t st)
 {
     const NormParams p = norm_params(qkv, bias, n, positions, kv_rows, T, Hq, Hkv, kv_rows_total, r);
-    // two tokens a CTA while that leaves no more CTAs than run at once, else eight
-    const bool few = T <= 2 * 4 * 148;
-    const int tok = few ? 2 : 8;
-    auto kern = few ? (r.interleaved ? qk_norm_fwd_kernel<true, 2> : qk_norm_fwd_kernel<false, 2>)
-                    : (r.interleaved ? qk_norm_fwd_kernel<true, 8> : qk_norm_fwd_kernel<false, 8>);
-    kern<<<(T + tok - 1) / tok, kThreads, 0, st>>>(p, static_cast<__nv_bfloat16 *>(q), static_cast<__nv_bfloat16 *>(k),
-                                                   static_cast<__nv_bfloat16 *>(v));
+    const int groups = head_groups(Hq + 2 * Hkv), slabs = num_slabs(T, groups, kFwdPerSm * 148);
+    auto kern = r.interleaved ? qk_norm_fwd_kernel<true> : qk_norm_fwd_kernel<false>;
+    constexpr int smem = kFwdRing * 2 * kThreads * 16;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(slabs * groups), kThreads, smem, st>>>(p, slabs, static_cast<__nv_bfloat16 *>(q),
+                                                             static_cast<__nv_bfloat16 *>(k),
+                                                             static_cast<__nv_bfloat16 *>(v));
     return cudaGetLastError();
 }
 
 size_t qk_norm_bwd_workspace_bytes(int T, int Hq, int Hkv)
 {
-    const size_t groups = head_groups(Hq + 2 * Hkv);
-    return (size_t)num_slabs(T) * groups * (kHeads + 2) * kD * sizeof(float);
+    const int groups = head_groups(Hq + 2 * Hkv);
+    return (size_t)num_slabs(T, groups, kBwdPerSm * 148) * groups * (kHeads + 2) * kD * sizeof(float);
 }
 
 cudaError_t launch_qk_norm_bwd(const void *qkv, const float *bias, const QkNorm &n, const int *positions,
@@ -492,8 +516,8 @@ cudaError_t launch_qk_norm_bwd(const void *qkv, const float *bias, const QkNorm 
     p.dqw = dq_weight;
     p.dkw = dk_weight;
     p.ws = ws;
-    p.slabs = num_slabs(T);
     p.groups = head_groups(Hq + 2 * Hkv);
+    p.slabs = num_slabs(T, p.groups, kBwdPerSm * 148);
     auto kern = r.interleaved ? qk_norm_bwd_kernel<true> : qk_norm_bwd_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     if (e != cudaSuccess) return e;
