@@ -191,11 +191,11 @@ TreeShape tree_shape(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, i
     // keys from the first one a root sees, rounded down to a tile, to the last drafted one
     const long long lw = window > 0 ? (long long)window - 1 + max_q + kTreeTile - 1 : (long long)Lmax;
     const long long lvis = lw < Lmax ? lw : Lmax;
-    long long splits = num_splits > 0 ? num_splits : 16 * 296 / ctas;
-    const long long least = num_splits > 0 ? kTreeTile : 256;
+    // (automatic: some sixteen CTAs an SM, each at least a tile of keys)
+    long long splits = num_splits > 0 ? num_splits : 16 * 148 / ctas;
     splits = splits < 1 ? 1 : (splits > kTreeMaxSplits ? kTreeMaxSplits : splits);
     long long chunk = (lvis + splits - 1) / splits;
-    chunk = ((chunk > least ? chunk : least) + kTreeTile - 1) / kTreeTile * kTreeTile;
+    chunk = (chunk + kTreeTile - 1) / kTreeTile * kTreeTile;
     s.chunk = (int)(chunk < 0x7fffffc0LL ? chunk : 0x7fffffc0LL);
     s.splits = (int)((lvis + s.chunk - 1) / s.chunk);
     return s;

@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
     grid_dep_launch();  // the combine may start its set-up; it waits for this grid
     __shared__ float qs[kRows][kD];
     __shared__ float ks[32][kD + 1];
-    __shared__ float vs[32][kD];
+    __shared__ __align__(16) float vs[32][kD];
     __shared__ int16_t par[kTreeMaxTokens], depth[kRows];
     __shared__ uint32_t path[kRows][kPathWords];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -90,11 +90,25 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
     const float C = s.scale * kLog2e;
     for (int j0 = kbeg; j0 < kend; j0 += 32) {
         __syncthreads();
-        for (int e = tid; e < 32 * kD; e += 128) {
-            const int j = j0 + e / kD;
-            const long long at = j < kend ? kv_offset(s, b, j, g) : -1;
-            ks[e / kD][e % kD] = at >= 0 ? kc[at + e % kD] : 0.f;
-            vs[e / kD][e % kD] = at >= 0 ? vc[at + e % kD] : 0.f;
+        {
+            // a quarter of a key's row a thread
+            const int jj = tid >> 2, d0 = (tid & 3) * 16;
+            const long long at = j0 + jj < kend ? kv_offset(s, b, j0 + jj, g) : -1;
+            float4 kv[4], vv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                kv[e] = at >= 0 ? *reinterpret_cast<const float4 *>(kc + at + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+                vv[e] = at >= 0 ? *reinterpret_cast<const float4 *>(vc + at + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float *k = &ks[jj][d0 + 4 * e];
+                k[0] = kv[e].x;
+                k[1] = kv[e].y;
+                k[2] = kv[e].z;
+                k[3] = kv[e].w;
+                *reinterpret_cast<float4 *>(&vs[jj][d0 + 4 * e]) = vv[e];
+            }
         }
         __syncthreads();
         const int j = j0 + lane, a = j - sq.cached;
