@@ -394,7 +394,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _call(where: str, dev: int, stream, *args):
     """Calls entry point `where` with device `dev` (the tensors') current: the library launches there."""
-    fn = getattr(load(), where)
+    fn = getattr(_lib or load(), where)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             rc = fn(*args, _stream(stream))

@@ -539,8 +539,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c_log2;
                 const bool move = big && tmax > m;
                 if (__any_sync(0xffffffffu, move)) {
-                    // up by a whole number of powers of two, so that the scaling is exact
-                    const float m_new = move ? (m == -INFINITY ? ceilf(tmax) : m + ceilf(tmax - m)) : m;
+                    // up by a whole number of powers of two, so that the scaling is exact (by more than 126, from
+                    // a sink far below or none: what was summed is 0 against the new reference)
+                    const float m_new = !move ? m : tmax - m > 126.f ? ceilf(tmax) : m + ceilf(tmax - m);
                     const float d = m_new - m;  // 0 where the reference stays, infinite where there was none
                     const float alpha = d > 126.f ? 0.f : __uint_as_float((uint32_t)(127 - (int)d) << 23);
                     m = m_new;

@@ -290,7 +290,7 @@ def test_tree_shapes(T, G, kind):
 
 @gpu
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("sink", [-math.inf, 60.0, -60.0])
+@pytest.mark.parametrize("sink", [-math.inf, 60.0, -60.0, -1e30, -3.4e38])
 def test_sinks_and_large_scores(sink, dtype):
     """No sink, a sink far above and far below the scores; scores that move the running maximum often."""
     c = make_case([400, 3], [9, 2], 8, 2, dtype, seed=15, std=4.0)
@@ -298,6 +298,8 @@ def test_sinks_and_large_scores(sink, dtype):
     c["k"][0, :400] *= torch.linspace(0.01, 1, 400)[:, None, None].to(dtype)  # growing scores
     for splits in (1, 3):
         check(c, run(c, 0, 0, splits), 0)
+    c["q"] *= 4  # scores in the hundreds: probabilities of one key
+    check(c, run(c, 0), 0)
 
 
 @gpu
@@ -420,3 +422,34 @@ def test_one_token_is_the_decode():
     check(c, (o2.cpu(), l2.cpu()), 0)
     check(c, (out, lse), 0)
     assert attn.attn_sink_get_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 6, 16, 60])
+def test_expired_waits_are_reported(T):
+    """With a limit of 1 ns the waits that outlast the hardware's own suspension of a try expire (2 GB of cache
+    that every CTA reads at once): the call winds down, the status says so once, and the next call with the
+    default limit is right.  (480 rows a KV head are bound by arithmetic, and no wait need be that long.)"""
+    B, L, Hkv = 64, 16384, 8
+    k = torch.zeros(B, L, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()
+    q = torch.zeros(B * T, 64, D, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(B * T, 64, device="cuda")
+    ws = torch.empty(attn.attn_sink_decode_tree_workspace_size(B, B * T, T, 64, Hkv, D, L, 0, 0, 1), dtype=torch.uint8,
+                     device="cuda")
+    args = (q, k, k.clone(), i32(range(0, B * T + 1, T)), i32([-1] * (B * T)), i32([L] * B),
+            torch.zeros(64, device="cuda"), out, lse, T, 0, 0.125, 0, ws)
+    old = attn.attn_sink_set_wait_timeout_ns(1)
+    try:
+        attn.attn_sink_decode_tree(*args)
+        status = attn.attn_sink_get_device_status()
+    finally:
+        attn.attn_sink_set_wait_timeout_ns(old)
+    assert status == -7 or (T == 60 and status == 0)
+    assert attn.attn_sink_get_device_status() == 0
+    attn.attn_sink_decode_tree(*args)
+    assert attn.attn_sink_get_device_status() == 0
+    # zero keys: every one of L - T cached and one drafted key, and the sink, weighs the same
+    assert (out == 0).all() and torch.allclose(lse, torch.tensor(math.log(L - T + 2.0), device="cuda"), atol=1e-5)
+    c = make_case([300, 500, 100], [T, T, 1], 16, 2, torch.bfloat16, seed=23)
+    check(c, run(c, 0), 0)
