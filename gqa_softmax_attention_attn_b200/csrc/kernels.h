@@ -150,7 +150,6 @@ struct TreeSeq {
     int len;         // cached keys, the computed drafted tokens' included
     int cached;      // keys in front of the drafted tokens' own
     int lo, lo_al;   // first key any of its rows sees; rounded down to a tile
-    int nsplit;      // chunks in use (at least one, which may be empty); fp32 path
 };
 __device__ __forceinline__ TreeSeq tree_seq(const TreeShape &s, int b)
 {
@@ -164,8 +163,12 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeShape &s, int b)
     // the shallowest position is the first behind the cached keys
     q.lo = s.window > 0 ? max(0, q.cached - s.window + 1) : 0;
     q.lo_al = q.lo / kTreeTile * kTreeTile;
-    q.nsplit = max(1, (q.len - q.lo_al + s.chunk - 1) / s.chunk);
     return q;
+}
+// fp32 path: chunks in use (at least one, which may be empty)
+__device__ __forceinline__ int tree_splits(const TreeShape &s, const TreeSeq &q)
+{
+    return max(1, (q.len - q.lo_al + s.chunk - 1) / s.chunk);
 }
 
 // Exact fp32 path (with the combine of its splits), and the tensor-core bf16 path.

@@ -65,8 +65,9 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
     const int g = rest % s.Hkv, c = rest / s.Hkv % s.splits, b = rest / s.Hkv / s.splits;
     const int G = s.Hq / s.Hkv;
     const TreeSeq sq = tree_seq(s, b);
+    const int nsplit = tree_splits(s, sq);
     const int rows = min(sq.T, s.max_q) * G, r0 = rt * kRows;
-    if (c >= sq.nsplit || r0 >= rows) return;  // uniform over the CTA
+    if (c >= nsplit || r0 >= rows) return;  // uniform over the CTA
     const int nrow = min(kRows, rows - r0);
     const int kbeg = max(sq.lo, sq.lo_al + c * s.chunk), kend = min(sq.len, sq.lo_al + (c + 1) * s.chunk);
 
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
         if (r >= rows) continue;
         const int h = g * G + r % G;
         const size_t at = (size_t)(sq.row0 + r / G) * s.Hq + h;
-        if (sq.nsplit == 1) {
+        if (nsplit == 1) {
             const float sk = s.sinks[h] * kLog2e, M = fmaxf(m[rr], sk);
             const float fo = m[rr] == -INFINITY ? 0.f : exp2f(m[rr] - M);
             const float L = l[rr] * fo + (sk == -INFINITY ? 0.f : exp2f(sk - M));
@@ -174,17 +175,18 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(float *__restrict__ o
                                                            const float *__restrict__ ws_ml, const TreeShape s)
 {
     const TreeSeq sq = tree_seq(s, blockIdx.y);
+    const int nsplit = tree_splits(s, sq);
     const int lane = threadIdx.x & 31;
     const int w = blockIdx.x * 4 + (threadIdx.x >> 5);  // (token, head) of the sequence
     grid_dep_wait();  // the partials of the grid ahead (programmatic dependent launch)
-    if (sq.nsplit <= 1 || w >= min(sq.T, s.max_q) * s.Hq) return;
+    if (nsplit <= 1 || w >= min(sq.T, s.max_q) * s.Hq) return;
     const size_t at = (size_t)sq.row0 * s.Hq + w, slot0 = at * s.splits;
     const float sk = s.sinks[w % s.Hq] * kLog2e;
     float mc[kTreeMaxSplits / 32], M = sk;
 #pragma unroll
     for (int k = 0; k < kTreeMaxSplits / 32; ++k) {
         const int c = 32 * k + lane;
-        mc[k] = c < sq.nsplit ? ws_ml[(slot0 + c) * 2] : -INFINITY;
+        mc[k] = c < nsplit ? ws_ml[(slot0 + c) * 2] : -INFINITY;
         M = fmaxf(M, mc[k]);
     }
     M = warp_max(M);
@@ -193,14 +195,14 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(float *__restrict__ o
     for (int k = 0; k < kTreeMaxSplits / 32; ++k) {
         const int c = 32 * k + lane;
         mc[k] = mc[k] == -INFINITY ? 0.f : exp2f(mc[k] - M);  // from here on the split's weight
-        if (c < sq.nsplit) L += ws_ml[(slot0 + c) * 2 + 1] * mc[k];
+        if (c < nsplit) L += ws_ml[(slot0 + c) * 2 + 1] * mc[k];
     }
     L = warp_sum(L) + (sk == -INFINITY ? 0.f : exp2f(sk - M));
     const float inv = L > 0.f ? 1.f / L : 0.f;
     float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
     for (int k = 0; k < kTreeMaxSplits / 32; ++k) {
-        const int n = min(32, sq.nsplit - 32 * k);
+        const int n = min(32, nsplit - 32 * k);
 #pragma unroll 4
         for (int c = 0; c < n; ++c) {
             const float f = __shfl_sync(0xffffffffu, mc[k], c);

@@ -97,6 +97,8 @@ constexpr int kTreeMinTiles = 4, kTreeSnapTiles = 8;
 struct TreeTcParams {
     TreeShape s;
     int G, row_tiles, copies, box_rows;
+    unsigned g_magic;   // ceil(2^32 / G), for row_token()
+    int page_shift;     // page_size = 2^page_shift, or -1
     int heads, head_groups;  // KV heads of a team; groups of them (units of the line) per sequence
     int teams;   // stretches of the line; a team is heads * row_tiles CTAs
     int q_min;   // shortest stretch, in tiles
@@ -109,6 +111,24 @@ struct TreeTcParams {
     unsigned *status;
     long long timeout_ns;
 };
+
+// Runtime divisions cost 100 cycles (32 bits) to 250 (64 bits), one after the other in front of a CTA's first
+// load; these are their cheap cases.
+__device__ __forceinline__ long long div64(long long a, long long b)
+{
+    return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+// row / G by the high word of row * ceil(2^32 / G): the product is off by row * (less than G), which stays below
+// 2^32 for rows and G below 2^16
+__device__ __forceinline__ int row_token(const TreeTcParams &p, int row)
+{
+    if (p.G == 1) return row;
+    return (row | p.G) >> 16 ? row / p.G : (int)__umulhi((unsigned)row, p.g_magic);
+}
+__device__ __forceinline__ int key_page(const TreeTcParams &p, int key)
+{
+    return p.page_shift >= 0 ? key >> p.page_shift : key / p.s.page_size;
+}
 
 // tiles of one unit of sequence b: the keys some row of it sees, at least one (a sequence without keys gets
 // its output from a tile that is masked altogether); none without rows
@@ -180,12 +200,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     };
 
     // ---- the plan: every CTA scans the batch's lengths (a thread a run of sequences) and takes its stretch
+    // (the barriers and tensor memory are set up meanwhile)
+    if (warp == 4 && lane == 0) {
+        for (int i = 0; i < kNS; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);  // the softmax warps
+        }
+        mbar_init(o_done, 1);
+        mbar_init(o_last, 1);
+        mbar_init(q_full, 4);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 6) {
+        tmem_alloc(tmem_slot, kTmCols);
+        tmem_relinquish();
+    }
     TreeSpan span;
     {
         const int run = (p.s.B + kThreads - 1) / kThreads;
         const int b0 = min((int)threadIdx.x * run, p.s.B), b1 = min(b0 + run, p.s.B);
         long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += (long long)unit_tiles(tree_seq(p.s, b)) * p.head_groups;
+        int nt0 = 0;  // of the thread's first sequence (its only one in batches of up to kThreads)
+        for (int b = b0; b < b1; ++b) {
+            const int nt = unit_tiles(tree_seq(p.s, b));
+            if (b == b0) nt0 = nt;
+            mine += (long long)nt * p.head_groups;
+        }
         long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -201,16 +248,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (w < warp) before += scan[w];
             total += scan[w];
         }
-        const long long q = max((total + p.teams - 1) / p.teams, (long long)p.q_min);
+        const long long q = max(div64(total + p.teams - 1, p.teams), (long long)p.q_min);
         const long long first = q * team, last = min(first + q, total);
         // (snap: the units that start in [first, last), whole)
         long long at = before;
         for (int b = b0; b < b1; ++b) {
-            const int nt = unit_tiles(tree_seq(p.s, b));
+            const int nt = b == b0 ? nt0 : unit_tiles(tree_seq(p.s, b));
             const long long len = (long long)nt * p.head_groups;
             if (blockIdx.x == 0 && p.plan) p.plan[1 + b] = at;
             if (first < last && at <= first && first < at + len) {
-                span_s->pos = p.snap ? at + (first - at + nt - 1) / nt * nt : first;
+                span_s->pos = p.snap ? at + div64(first - at + nt - 1, nt) * nt : first;
                 span_s->end = last;
                 span_s->base = at;
                 span_s->b = b;
@@ -221,12 +268,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             p.plan[0] = q;
             p.plan[1 + p.s.B] = total;
         }
+        tc_fence_before();
         __syncthreads();
+        tc_fence_after();
         span = *span_s;
-        if (span.b < 0) return;  // no work: uniform over the CTA
     }
+    const uint32_t tmem = *tmem_slot;
     // segment by segment: f(sequence, its number, KV head, first tile, tiles, all tiles of the unit); stops at false
     auto for_segments = [&](auto f) {
+        if (span.b < 0) return;  // no work
         long long pos = span.pos, base = span.base;
         int b = span.b;
         TreeSeq sq = tree_seq(p.s, b);
@@ -237,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 sq = tree_seq(p.s, ++b);
                 nt = unit_tiles(sq);
             }
-            const int g = (int)((pos - base) / nt) * p.heads + head, ta = (int)((pos - base) % nt);
+            const int u = p.head_groups == 1 ? 0 : (int)div64(pos - base, nt);
+            const int g = u * p.heads + head, ta = (int)(pos - base - (long long)u * nt);
             const int n = p.snap ? nt : (int)min((long long)(nt - ta), span.end - pos);
             if (r0 < min(sq.T, p.s.max_q) * p.G && !f(sq, b, g, ta, n, nt, pos == span.pos)) return;
             pos += n;
@@ -257,11 +308,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // the pages of 32 boxes from tile t of the segment on, one a lane; boxes behind the sequence
             // (masked) reuse its last page, so the table is only read within the sequence's own entries
             auto pages = [&](int t) -> int {
-                const int lp = (key0 + t * kBN + lane * p.box_rows) / ps;
-                return p.s.page_table[(size_t)b * p.s.max_pages + min(lp, max(sq.len - 1, 0) / ps)];
+                const int lp = key_page(p, min(key0 + t * kBN + lane * p.box_rows, max(sq.len - 1, 0)));
+                return p.s.page_table[(size_t)b * p.s.max_pages + lp];
             };
             // a tile's slot in its page: 0 for pages of at most a tile, else it advances with the tiles
-            int slot = ps > 0 ? key0 % ps : key0, in_batch = 0;
+            int slot = ps > 0 ? key0 - key_page(p, key0) * ps : key0, in_batch = 0;
             int page = 0, next_page = 0;
             if (ps > 0) {
                 page = pages(0);
@@ -307,32 +358,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int x = 0; x < kNS && x < pt; ++x)
             wait_noabort(&full[x], (uint32_t)((pt - 1 - x) / kNS) & 1u, p.status, p.timeout_ns);
     };
-
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kNS; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);  // the softmax warps
-        }
-        mbar_init(o_done, 1);
-        mbar_init(o_last, 1);
-        mbar_init(q_full, 4);
-        *abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 6) {
-        tmem_alloc(tmem_slot, kTmCols);
-        tmem_relinquish();
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
 
     if (warp == 4) {
         produce(tmK, k_full, k_empty, smem_u32(smem + kOffK));
@@ -443,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int k = 0; k < 16; ++k) z[k] = 0u;
 #pragma unroll
             for (int k = 0; k < kBN / 16; ++k) tmem_st16(trow + kTmP + 16 * k, z);
+            tmem_wait_st();
         }
         const float2 C2 = make_float2(p.c_log2, p.c_log2);
         uint32_t n = 0, n_seg = 0;  // tiles, segments so far
@@ -450,9 +476,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int rows = min(sq.T, p.s.max_q) * p.G, nrow = min(kRows, rows - r0);
         const bool valid = r < nrow;
         const bool active = (warp * 32) % kRows < nrow;  // some row of this warp exists
-        const int row = r0 + (valid ? r : 0);
-        const int i0 = r0 / p.G, tok = row / p.G - i0, h = g * p.G + row % p.G;
-        const size_t at = (size_t)(sq.row0 + row / p.G) * p.s.Hq + h;
+        const int row = r0 + (valid ? r : 0), row_tok = row_token(p, row);
+        const int i0 = row_token(p, r0), tok = row_tok - i0, h = g * p.G + row - row_tok * p.G;
+        const size_t at = (size_t)(sq.row0 + row_tok) * p.s.Hq + h;
         {
             // Q: this thread's row into the 128-byte-swizzled operand tile (rows that do not exist: zeros)
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * kD);
@@ -473,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         float l = 0.f;   // running sum, without the sink
         int vis_lo = 0;  // first cached key this row sees
         if (p.s.window > 0 || kfirst + nt * kBN > sq.cached) {
-            tree_paths(p.s, sq, i0, (r0 + nrow - 1) / p.G - i0 + 1, lrow, 128,
+            tree_paths(p.s, sq, i0, row_token(p, r0 + nrow - 1) - i0 + 1, lrow, 128,
                        reinterpret_cast<int16_t *>(smem + kOffPar), path, depth, [] { named_bar_sync(1, 128); });
             if (p.s.window > 0) vis_lo = max(0, sq.cached + depth[tok] - p.s.window + 1);
         }
@@ -707,15 +733,17 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeTcParams p)
     const int w = blockIdx.x * 4 + (threadIdx.x >> 5);  // (token, head) of the sequence
     const SeqRows sr = seq_rows(p.s.cu_q, b, 0, p.s.total_q);
     if (w >= min(sr.len, p.s.max_q) * p.s.Hq) return;
-    const int h = w % p.s.Hq, g = h / p.G, row = w / p.s.Hq * p.G + h % p.G;
-    const int per_tile = kM / p.copies, rt = row / per_tile, r = row % per_tile;
-    const long long q = p.plan[0], base = p.plan[1 + b], nt = (p.plan[2 + b] - base) / p.head_groups;
-    const long long u0 = base + g / p.heads * nt;                      // the unit's first tile
-    const int j0 = (int)(u0 / q), j1 = (int)((u0 + nt - 1) / q);  // the teams it was cut over
+    const int tok = w / p.s.Hq, h = w - tok * p.s.Hq, g = row_token(p, h), row = tok * p.G + h - g * p.G;
+    const int per_tile = kM / p.copies, rt = row / per_tile, r = row - rt * per_tile;
+    const int team_head = p.head_groups == 1 ? g : g % p.heads;
+    const long long q = p.plan[0], base = p.plan[1 + b], all = p.plan[2 + b] - base;
+    const long long nt = p.head_groups == 1 ? all : div64(all, p.head_groups);
+    const long long u0 = base + (p.head_groups == 1 ? 0 : g / p.heads * nt);  // the unit's first tile
+    const int j0 = (int)div64(u0, q), j1 = (int)div64(u0 + nt - 1, q);        // the teams it was cut over
     if (j0 == j1) return;  // written in one piece
     auto slot = [&](int j) -> size_t {
-        const int second = j == j0 && u0 % q != 0;  // not the first segment of its CTA
-        return ((size_t)((j * p.heads + g % p.heads) * p.row_tiles + rt) * 2 + second) * per_tile + r;
+        const int second = j == j0 && u0 != j0 * q;  // not the first segment of its CTA
+        return ((size_t)((j * p.heads + team_head) * p.row_tiles + rt) * 2 + second) * per_tile + r;
     };
     const float sk = p.s.sinks[h] * kLog2e;
     float M = sk;
@@ -808,6 +836,10 @@ cudaError_t launch_tree_tc(const void *q, const void *kc, const void *vc, void *
     TreeTcParams p;
     p.s = s;
     p.G = s.Hq / s.Hkv;
+    p.g_magic = p.G > 1 ? (unsigned)((0x100000000ull + p.G - 1) / p.G) : 0;
+    p.page_shift = -1;
+    for (int x = 3; x < 31; ++x)
+        if (s.page_size == 1 << x) p.page_shift = x;
     p.copies = t.copies;
     p.row_tiles = t.row_tiles;
     p.heads = t.heads;
