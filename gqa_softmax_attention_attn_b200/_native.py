@@ -361,10 +361,12 @@ def attn_sink_bwd(q, k, v, sinks, out, dout, lse, dq, dk, dv, dsinks, window: in
 
 def _take(t, name: str, dtype, shape, dev: int) -> int:
     """The data pointer of a contiguous tensor of this dtype and shape on device `dev`."""
-    if (not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.get_device() != dev or dev < 0
-            or not t.is_contiguous()):
-        _refuse(t, name, dtype, shape, dev)
-    return t.data_ptr()
+    try:
+        if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, dev)
 
 
 def _refuse(t, name, dtype, shape, dev):
@@ -394,6 +396,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _call(where: str, dev: int, stream, *args):
     """Calls entry point `where` with device `dev` (the tensors') current: the library launches there."""
+    if dev < 0:
+        raise ValueError(f"{where}: the tensors must be CUDA tensors")
     fn = getattr(_lib or load(), where)
     if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
@@ -430,8 +434,8 @@ def attn_sink_decode_tree(q, k_cache, v_cache, cu_seqlens_q, parents, seqlens, s
     keys as the last of seqlens [B] int32 -> writes out [total_q,Hq,D], lse [total_q,Hq]."""
     (total_q, Hq, D), (B, Lmax, Hkv, _), dev = q.shape, k_cache.shape, q.get_device()
     args = _tree_args(q, (k_cache, v_cache), (B, Lmax, Hkv, D), (), B, cu_seqlens_q, parents, seqlens, sinks, out, lse)
-    _call("attn_sink_decode_tree", dev, stream, *args, B, total_q, max_seqlen_q, Lmax, Hq, Hkv, D, window, scale,
-          num_splits, *_take_workspace(workspace, dev), _dtype_code(q))
+    _call("attn_sink_decode_tree", dev, stream, *args, B, total_q, int(max_seqlen_q), Lmax, Hq, Hkv, D, int(window),
+          float(scale), int(num_splits), *_take_workspace(workspace, dev), _dtype_code(q))
 
 
 def attn_sink_decode_tree_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, parents, seqlens, sinks, out, lse,
@@ -444,8 +448,9 @@ def attn_sink_decode_tree_paged(q, k_pages, v_pages, page_table, cu_seqlens_q, p
     table = _take(page_table, "page_table", torch.int32, (B, max_pages), dev)
     args = _tree_args(q, (k_pages, v_pages), (num_pages, page_size, Hkv, D), (table,), B, cu_seqlens_q, parents,
                       seqlens, sinks, out, lse)
-    _call("attn_sink_decode_tree_paged", dev, stream, *args, B, total_q, max_seqlen_q, max_pages, page_size, num_pages,
-          Hq, Hkv, D, window, scale, num_splits, *_take_workspace(workspace, dev), _dtype_code(q))
+    _call("attn_sink_decode_tree_paged", dev, stream, *args, B, total_q, int(max_seqlen_q), max_pages, page_size,
+          num_pages, Hq, Hkv, D, int(window), float(scale), int(num_splits), *_take_workspace(workspace, dev),
+          _dtype_code(q))
 
 
 def attn_sink_page_map(cached_lens, new_lens, free_pages, page_table, seqlens, cu_seqlens, positions, kv_rows, stats,
@@ -464,7 +469,7 @@ def attn_sink_page_map(cached_lens, new_lens, free_pages, page_table, seqlens, c
           _take(page_table, "page_table", i32, (B, max_pages), dev), _take(seqlens, "seqlens", i32, (B,), dev),
           _take(cu_seqlens, "cu_seqlens", i32, (B + 1,), dev), _take(positions, "positions", i32, (total,), dev),
           _take(kv_rows, "kv_rows", i32, (total,), dev), _take(stats, "stats", i32, (4,), dev), B, total, max_pages,
-          page_size, num_pages, n_free)
+          int(page_size), int(num_pages), n_free)
 
 
 def attn_sink_qk_norm_prologue(qkv, bias, q_weight, k_weight, positions, q_out, k_out, v_out, eps: float,
@@ -482,8 +487,9 @@ def attn_sink_qk_norm_prologue(qkv, bias, q_weight, k_weight, positions, q_out, 
           _take(positions, "positions", i32, (T,), dev),
           _take(kv_rows, "kv_rows", i32, (T,), dev) if kv_rows is not None else None,
           _take(q_out, "q_out", bf, (T, Hq, D), dev), _take(k_out, "k_out", bf, (rows, Hkv, D), dev),
-          _take(v_out, "v_out", bf, (rows, Hkv, D), dev), T, Hq, Hkv, D, rows, eps, rope_theta, rope_factor,
-          rope_original_max_pos, beta_fast, beta_slow, int(bool(interleaved)))
+          _take(v_out, "v_out", bf, (rows, Hkv, D), dev), T, Hq, Hkv, D, rows, float(eps),
+          float(rope_theta), float(rope_factor), int(rope_original_max_pos), float(beta_fast), float(beta_slow),
+          int(bool(interleaved)))
 
 
 def attn_sink_qk_norm_prologue_bwd_workspace_size(T: int, Hq: int, Hkv: int, D: int) -> int:
@@ -507,8 +513,8 @@ def attn_sink_qk_norm_prologue_bwd(qkv, bias, q_weight, k_weight, positions, dq,
           _take(dk, "dk", bf, (T, Hkv, D), dev), _take(dv, "dv", bf, (T, Hkv, D), dev),
           _take(dqkv, "dqkv", bf, (T, W), dev), _take(dbias, "dbias", f32, (W,), dev) if dbias is not None else None,
           _take(dq_weight, "dq_weight", f32, (D,), dev), _take(dk_weight, "dk_weight", f32, (D,), dev), T, Hq, Hkv, D,
-          eps, rope_theta, rope_factor, rope_original_max_pos, beta_fast, beta_slow, int(bool(interleaved)),
-          *_take_workspace(workspace, dev))
+          float(eps), float(rope_theta), float(rope_factor), int(rope_original_max_pos), float(beta_fast),
+          float(beta_slow), int(bool(interleaved)), *_take_workspace(workspace, dev))
 
 
 def attn_sink_get_device_status(stream=None) -> int:
