@@ -386,12 +386,16 @@ def _refuse(t, name, dtype, shape, dev):
 def _take_workspace(workspace, dev: int):
     if workspace is None:
         return None, 0
-    nbytes = workspace.numel() * workspace.element_size()
-    return _take(workspace, "workspace", workspace.dtype, workspace.shape, dev), nbytes
+    if not isinstance(workspace, torch.Tensor):
+        raise ValueError("workspace must be a CUDA tensor")
+    if workspace.get_device() == dev and workspace.is_contiguous():
+        return workspace.data_ptr(), workspace.nbytes
+    _refuse(workspace, "workspace", workspace.dtype, workspace.shape, dev)
 
 
 # the current stream's handle without building a Stream object (3 us less a call)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(where: str, dev: int, stream, *args):
@@ -399,7 +403,7 @@ def _call(where: str, dev: int, stream, *args):
     if dev < 0:
         raise ValueError(f"{where}: the tensors must be CUDA tensors")
     fn = getattr(_lib or load(), where)
-    if torch.cuda.current_device() != dev:
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             rc = fn(*args, _stream(stream))
     elif stream is None and _raw_stream is not None:
