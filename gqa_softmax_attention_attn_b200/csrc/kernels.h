@@ -191,8 +191,8 @@ struct RopeParams {
     double base, factor, original_max_pos, beta_fast, beta_slow;
     int interleaved;  // 0: pairs (i, i + D/2); 1: pairs (2i, 2i + 1)
 };
-// rotary frequency of pair i after the YaRN correction, and the factor on cos and sin (host)
-double rope_frequency(const RopeParams &r, int i);
+// rotary frequencies of the D / 2 pairs after the YaRN correction, and the factor on cos and sin (host)
+void rope_frequencies(const RopeParams &r, double *f);
 double rope_attention_factor(const RopeParams &r);
 
 // The prologue with RMS norms of every q and k head in front of the rotation, and its backward.
