@@ -195,6 +195,25 @@ struct RopeParams {
 void rope_frequencies(const RopeParams &r, double *f);
 double rope_attention_factor(const RopeParams &r);
 
+// Launches kern as the dependent of the grid ahead on the stream (programmatic dependent launch): it may start
+// while that grid still runs, once all of its CTAs have started and allowed it, and touches global memory only
+// behind its own grid_dep_wait(), which every one of its threads reaches first.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // The prologue with RMS norms of every q and k head in front of the rotation, and its backward.
 struct QkNorm {
     const float *q_weight, *k_weight;  // [D] fp32

@@ -16,9 +16,11 @@
 // by a binary search of the scanned offsets in shared memory.  CTA 0 writes
 // the per-request results, and the new pages' entries are dealt out evenly.
 // Bound by latency: two dependent trips to L2, a scan over the CTA and a search
-// of 10 steps.  64 requests of 8 tokens 5.1 us on the device, 1000 requests of
-// mixed lengths 6.2 us (back to back from a graph).
+// of 10 steps.  64 requests of 8 tokens 4.9 us on the device, 1000 requests of
+// mixed lengths 5.7 us (back to back from a graph; 7.0 us with the next grid let in early, whose
+// waiting CTAs then share the SMs with this one's).
 #include "kernels.h"
+#include "sm100_ptx.cuh"
 
 namespace attn_sink {
 namespace {
@@ -71,6 +73,7 @@ __global__ void __launch_bounds__(kThreads) page_map_kernel(const MapParams p)
     __shared__ int par[kTreeMaxTokens + kTokens];
     __shared__ long long wsum[kThreads / 32];
     __shared__ int wtake[kThreads / 32], wover[kThreads / 32];
+    grid_dep_wait();  // the grid ahead
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int t0 = blockIdx.x * kTokens;
     const int ps = p.s.page_size;
@@ -213,8 +216,7 @@ cudaError_t launch_page_map(const int *cached_lens, const int *new_lens, const i
 {
     const MapParams p{s, cached_lens, new_lens, parents, free_pages, page_table, seqlens, cu_seqlens, positions,
                       kv_rows, stats};
-    page_map_kernel<<<(s.total_tokens - 1) / kTokens + 1, kThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    return launch_chained(page_map_kernel, dim3((unsigned)((s.total_tokens - 1) / kTokens + 1)), kThreads, 0, st, p);
 }
 
 }  // namespace attn_sink

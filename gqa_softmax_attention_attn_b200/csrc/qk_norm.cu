@@ -17,12 +17,13 @@
 // rotation needs no exchange and a sum over the head is two shuffles.
 //
 // Bound by HBM and instruction issue together (64 + 8 + 8 heads): forward of
-// 4096 tokens 17.7 us, 4.7 TB/s; of 16384 tokens 63 us under a profiler, 4.6 TB/s
+// 4096 tokens 17.3 us, 4.8 TB/s; of 16384 tokens 63 us under a profiler, 4.6 TB/s
 // of DRAM with 60 % of the issue slots taken; backward of 65536 tokens 359 us, 5.6 TB/s (406
 // in runs of seconds, at the power limit, the clock down to 1.73 GHz); of 1003
 // tokens 10.8 us, two launches and the latency of one slab.  Two pairs per
 // instruction, the asynchronous ring and slabs as many as run at once brought
-// 4096 tokens from 26.6 us and 65536 tokens backward from 614 us.
+// 4096 tokens from 26.6 us and 65536 tokens backward from 614 us; starting while
+// the grid ahead ends took 512 tokens from 4.5 to 4.1 us.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -206,6 +207,8 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const 
                                                                           __nv_bfloat16 *__restrict__ k,
                                                                           __nv_bfloat16 *__restrict__ v)
 {
+    grid_dep_launch();
+    grid_dep_wait();  // the grid ahead
     __shared__ __align__(16) float rot[2][kBTok][2 * kPairs];
     extern __shared__ __align__(16) uint8_t ring_raw[];  // [kFwdRing][2 chunks][kThreads] of 16 bytes
     const int heads = p.Hq + 2 * p.Hkv, groups = head_groups(heads);
@@ -299,7 +302,8 @@ constexpr int kBwdSmem = kRing * 4 * kThreads * 16;
 template <bool kInter>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) qk_norm_bwd_kernel(const BwdParams bp)
 {
-    grid_dep_launch();
+    grid_dep_launch();  // the finish kernel may start; it waits for this grid
+    grid_dep_wait();    // (as this one for the grid ahead)
     const NormParams &p = bp.n;
     __shared__ __align__(16) float rot[2][kBTok][2 * kPairs];
     extern __shared__ __align__(16) uint8_t ring_raw[];  // [kRing][4 chunks][kThreads] of 16 bytes
@@ -443,6 +447,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_finish_kernel(const BwdParam
     const float *src = which < 0 ? bp.ws + (size_t)blockIdx.x * kD : bp.ws + bp.slabs * wide + which * kD;
     const size_t stride = which < 0 ? wide : 2 * kD;
     const int n = which < 0 ? bp.slabs : bp.slabs * bp.groups;
+    grid_dep_launch();
     grid_dep_wait();
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -498,10 +503,9 @@ cudaError_t launch_qk_norm_prologue(const void *qkv, const float *bias, const Qk
     constexpr int smem = kFwdRing * 2 * kThreads * 16;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(slabs * groups), kThreads, smem, st>>>(p, slabs, static_cast<__nv_bfloat16 *>(q),
-                                                             static_cast<__nv_bfloat16 *>(k),
-                                                             static_cast<__nv_bfloat16 *>(v));
-    return cudaGetLastError();
+    return launch_chained(kern, dim3((unsigned)(slabs * groups)), kThreads, smem, st, p, slabs,
+                          static_cast<__nv_bfloat16 *>(q), static_cast<__nv_bfloat16 *>(k),
+                          static_cast<__nv_bfloat16 *>(v));
 }
 
 size_t qk_norm_bwd_workspace_bytes(int T, int Hq, int Hkv)
@@ -530,19 +534,9 @@ cudaError_t launch_qk_norm_bwd(const void *qkv, const float *bias, const QkNorm 
     auto kern = r.interleaved ? qk_norm_bwd_kernel<true> : qk_norm_bwd_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     if (e != cudaSuccess) return e;
-    kern<<<p.slabs * p.groups, kThreads, kBwdSmem, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_chained(kern, dim3((unsigned)(p.slabs * p.groups)), kThreads, kBwdSmem, st, p);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((dbias ? Hq + 2 * Hkv : 0) + 2));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qk_norm_finish_kernel, p);
+    return launch_chained(qk_norm_finish_kernel, dim3((unsigned)((dbias ? Hq + 2 * Hkv : 0) + 2)), kThreads, 0, st, p);
 }
 
 }  // namespace attn_sink

@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
                                                         float *__restrict__ ws_ml, const TreeShape s, int row_tiles)
 {
     grid_dep_launch();  // the combine may start its set-up; it waits for this grid
+    grid_dep_wait();    // (as this one for the grid ahead)
     __shared__ float qs[kRows][kD];
     __shared__ float ks[32][kD + 1];
     __shared__ __align__(16) float vs[32][kD];
@@ -177,11 +178,11 @@ __global__ void __launch_bounds__(128) tree_combine_kernel(float *__restrict__ o
                                                            const float *__restrict__ ws_o,
                                                            const float *__restrict__ ws_ml, const TreeShape s)
 {
+    grid_dep_wait();  // the partials of the grid ahead (programmatic dependent launch)
     const TreeSeq sq = tree_seq(s, blockIdx.y);
     const int nsplit = tree_splits(s, sq);
     const int lane = threadIdx.x & 31;
     const int w = blockIdx.x * 4 + (threadIdx.x >> 5);  // (token, head) of the sequence
-    grid_dep_wait();  // the partials of the grid ahead (programmatic dependent launch)
     if (nsplit <= 1 || w >= min(sq.T, s.max_q) * s.Hq) return;
     const size_t at = (size_t)sq.row0 * s.Hq + w, slot0 = at * s.splits;
     const float sk = s.sinks[w % s.Hq] * kLog2e;
@@ -226,19 +227,11 @@ cudaError_t launch_tree_simt(const float *q, const float *kc, const float *vc, f
     const int row_tiles = (s.max_q * (s.Hq / s.Hkv) + kRows - 1) / kRows;
     const long long ctas = (long long)row_tiles * s.Hkv * s.splits * s.B;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    tree_simt_kernel<<<(unsigned)ctas, 128, 0, st>>>(q, kc, vc, out, lse, ws_o, ws_ml, s, row_tiles);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_chained(tree_simt_kernel, dim3((unsigned)ctas), 128, 0, st, q, kc, vc, out, lse, ws_o,
+                                         ws_ml, s, row_tiles);
     if (e != cudaSuccess || s.splits <= 1) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)s.max_q * s.Hq + 3) / 4), (unsigned)s.B);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_combine_kernel, out, lse, (const float *)ws_o, (const float *)ws_ml, s);
+    return launch_chained(tree_combine_kernel, dim3((unsigned)(((long long)s.max_q * s.Hq + 3) / 4), (unsigned)s.B), 128,
+                          0, st, out, lse, (const float *)ws_o, (const float *)ws_ml, s);
 }
 
 }  // namespace attn_sink

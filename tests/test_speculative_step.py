@@ -113,3 +113,85 @@ def test_steps_of_a_server(window):
             for ref in (ref_k, ref_v):
                 ref[b] = np.concatenate([ref[b][:cached[b]], ref[b][cached[b]:][path]])
     assert attn.attn_sink_get_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_calls_in_line(dtype):
+    """Every call's kernels may start while the grid ahead still runs: a line of calls that each read what the
+    one before wrote, and write what it read, gives the bits of the same calls with a synchronisation after each,
+    run eagerly and from a captured graph."""
+    B, T, pages, width = 4, 10, 80, 20
+    n = B * T
+    g = torch.Generator().manual_seed(31)
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()
+    dev = dict(device="cuda")
+    qkv0 = torch.randn(n, (Hq + 2 * Hkv) * D, generator=g).bfloat16().cuda()
+    pool0 = torch.randn(2, pages, PS, Hkv, D, generator=g).to(dtype).cuda()
+    bias = (torch.randn((Hq + 2 * Hkv) * D, generator=g) * 0.1).cuda()
+    qw, kw = (1 + 0.2 * torch.randn(D, generator=g)).cuda(), (1 + 0.2 * torch.randn(D, generator=g)).cuda()
+    sinks = torch.randn(Hq, generator=g).cuda()
+    parents = i32(sum((make_tree(T, "random", g) for _ in range(B)), []))
+    free = i32(torch.randperm(pages, generator=g))
+    ws = torch.empty(max(16, attn.attn_sink_decode_tree_workspace_size(
+        B, n, T, Hq, Hkv, D, width * PS, 0, 0, attn.DTYPE_BF16 if dtype == torch.bfloat16 else attn.DTYPE_F32)),
+        dtype=torch.uint8, **dev)
+    ws_bwd = torch.empty(attn.attn_sink_qk_norm_prologue_bwd_workspace_size(n, Hq, Hkv, D), dtype=torch.uint8, **dev)
+    cached, new = i32([250, 0, 17, 100]), i32([T] * B)
+
+    class State:
+        pass
+
+    def fresh():
+        s = State()
+        s.qkv, s.table = qkv0.clone(), torch.full((B, width), -1, dtype=torch.int32, **dev)
+        have = [(c + PS - 1) // PS for c in cached.tolist()]
+        for b in range(B):  # pages already held: the last ones of the list
+            s.table[b, :have[b]] = free[pages - sum(have[:b + 1]):pages - sum(have[:b])]
+        s.k, s.v = pool0[0].clone(), pool0[1].clone()
+        s.kt, s.vt = (torch.empty(n, Hkv, D, dtype=torch.bfloat16, **dev) for _ in range(2))
+        s.lens, s.cu, s.pos, s.rows, s.stats = (torch.zeros(x, dtype=torch.int32, **dev) for x in (B, B + 1, n, n, 4))
+        s.q = torch.empty(n, Hq, D, dtype=torch.bfloat16, **dev)
+        s.out, s.lse = torch.empty(n, Hq, D, dtype=dtype, **dev), torch.empty(n, Hq, **dev)
+        s.dqkv, s.dbias = torch.empty_like(s.qkv), torch.empty_like(bias)
+        s.dqw, s.dkw = torch.empty_like(qw), torch.empty_like(kw)
+        return s
+
+    def line(s, after=lambda: None):
+        x, y = s.qkv, s.dqkv
+        for _ in range(4):
+            attn.attn_sink_page_map(cached, new, free, s.table, s.lens, s.cu, s.pos, s.rows, s.stats, PS, pages,
+                                    parents=parents)
+            after()
+            if dtype == torch.bfloat16:
+                attn.attn_sink_qk_norm_prologue(x, bias, qw, kw, s.pos, s.q, s.k.view(-1, Hkv, D),
+                                                s.v.view(-1, Hkv, D), EPS, kv_rows=s.rows, **YARN)
+                after()
+            attn.attn_sink_qk_norm_prologue(x, bias, qw, kw, s.pos, s.q, s.kt, s.vt, EPS, **YARN)
+            after()
+            a, b = s.q if dtype == torch.bfloat16 else s.q.float(), s.out
+            for _ in range(3):  # each on the output of the one before
+                attn.attn_sink_decode_tree_paged(a, s.k, s.v, s.table, s.cu, parents, s.lens, sinks, b, s.lse, T, 0,
+                                                 0.125, 0, ws)
+                after()
+                a, b = b, a
+            attn.attn_sink_qk_norm_prologue_bwd(x, bias, qw, kw, s.pos, s.q, s.kt, s.vt, y, s.dbias, s.dqw, s.dkw, EPS,
+                                                workspace=ws_bwd, **YARN)
+            after()
+            x, y = y, x
+        return x, s.out, s.lse, s.k, s.v, s.dbias, s.dqw, s.dkw, s.pos, s.rows, s.table
+
+    want = [t.clone() for t in line(fresh(), torch.cuda.synchronize)]
+    assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+    for _ in range(3):
+        for a, b in zip(line(fresh()), want):
+            assert torch.equal(a, b)
+    s = fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = line(s)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert attn.attn_sink_get_device_status() == 0
