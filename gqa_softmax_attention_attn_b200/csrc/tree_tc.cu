@@ -33,10 +33,10 @@
 //    which it has plenty to spare while HBM is the limit.
 //  * Warps 0-3, one row (copy) a thread, do the softmax; warps 4 and 5 stream K and
 //    V in tiles of 64 keys (128-byte-swizzled TMA boxes, one a page for small
-//    pages) through rings of kNS stages; warp 6 issues S = Q K^T and O += P V, both S and P
-//    double-buffered in tensor memory, so that neither product is in the
+//    pages) through rings of kNS stages; warp 6 issues S = Q K^T and O += P V, Q and P read from
+//    tensor memory, S double-buffered there, so that neither product is in the
 //    softmax warps' chain: S(t + 2) follows P V(t).  One warp issues both, in order, so S(t + 2) being
-//    complete means P V(t) is, and its P buffer free, without another wait.
+//    complete means P V(t) is.
 //    (Four chains an SM with single buffers, P written over S, hid less: from P
 //    to the next S 1000 to 1700 cycles a tile were in each chain, 1060 cycles a
 //    tile and SM in all.)
@@ -55,11 +55,11 @@
 // for seconds it takes 425 to 475 us: HBM, the products and the exponentials
 // together reach the 1000 W limit and the clock falls to 1.2 to 1.4 GHz (without
 // the products 360 us).  Beyond 64 rows a KV head the softmax warps' chain
-// bounds it: 16 sequences of 61 tokens 205 us, one of 131072 keys with 32 tokens 121
+// bounds it: 16 sequences of 61 tokens 202 us, one of 131072 keys with 32 tokens 119
 // us; a tile is 1500 cycles of it, 880 in the pass of the exponentials (two CTAs'
 // warps share a scheduler; 440 without the exponentials) and 600 in its waits, votes,
-// loads and arrivals, 90 to 180 each.  (Not bounded by the S products: with three S buffers, P
-// over S, 201 us; nor by the load of S: with the next tile's scores loaded during the pass 225 us.)
+// loads and arrivals, 90 to 180 each.  (Not bounded by the S products: with three S buffers
+// 201 us; nor by the load of S: with the next tile's scores loaded during the pass 225 us.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -83,8 +83,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSumLimit = 1024.f;
 
 constexpr int kTileBytes = kBN * kD * 2;
-constexpr int kOffQ = 0;
-constexpr int kOffK = kM * kD * 2;
+constexpr int kOffRed = 0;  // [128][32] half of the copies' O, joined after the last tile
+constexpr int kOffK = kM * 32 * 4;
 constexpr int kOffV = kOffK + kNS * kTileBytes;
 constexpr int kOffPath = kOffV + kNS * kTileBytes;         // [128][kPathWords] ancestor bits
 constexpr int kOffDepth = kOffPath + kM * kPathWords * 4;  // [128] depths
@@ -98,9 +98,11 @@ constexpr int kOffMisc = kOffPlan + 32 + 8 * 8;             // TMEM address, abo
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
 static_assert(kOffBar % 8 == 0, "barriers on 8 bytes");
 static_assert(kCtasPerSm * (kSmemBytes + 1024) <= 228 * 1024, "shared memory");
-// tensor memory: S and P (bf16) double-buffered, O
-constexpr int kTmS = 0, kTmP = 2 * kBN, kTmO = kTmP + kBN, kTmCols = 256;
-static_assert(kTmO + kD <= kTmCols && kCtasPerSm * kTmCols <= 512, "tensor memory");
+// tensor memory: S double-buffered, O, Q (bf16, 32 columns), and P (bf16): over S with one copy of the rows (the
+// tensor pipe runs one thread's MMAs in order, so the next S there follows P V), else a buffer of its own, whose
+// zeros in the other copies' keys stay
+constexpr int kTmS = 0, kTmO = 2 * kBN, kTmQ = kTmO + kD, kTmP = kTmQ + kD / 2, kTmCols = 256;
+static_assert(kTmP + kBN / 2 <= kTmCols && kCtasPerSm * kTmCols <= 512, "tensor memory");
 // shortest stretch of the line; units up to kTreeSnapTiles are never cut
 constexpr int kTreeMinTiles = 4, kTreeSnapTiles = 8;
 
@@ -377,7 +379,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     } else if (warp == 6) {
         // ------------------------------------------------------------ MMA issuer (converged, one lane issues)
         constexpr uint32_t id_s = idesc_bf16_f32(kM, kBN, 0), id_pv = idesc_bf16_f32(kM, kD, 1);
-        const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + kOffQ), 16, 1024);
         const uint64_t k_desc = smem_desc_sw128(smem_u32(smem + kOffK), 16, 1024);
         const uint64_t v_desc = smem_desc_sw128(smem_u32(smem + kOffV), kBN * 128, 1024);
         int kst = 0, st = 0;  // stages of the next K, of the next V, and their phases
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             const uint32_t ts = tmem + kTmS + (sn & 1) * kBN;
 #pragma unroll
             for (int kk = 0; kk < kD / 16; ++kk)
-                mma_ss(ts, q_desc + (uint64_t)(kk * 32 >> 4), kd + (uint64_t)(kk * 32 >> 4), id_s, kk > 0 ? 1u : 0u);
+                mma_ts(ts, tmem + kTmQ + kk * 8, kd + (uint64_t)(kk * 32 >> 4), id_s, kk > 0 ? 1u : 0u);
             mma_commit(&s_full[sn & 1]);
             mma_commit(&k_empty[kst]);
         };
@@ -403,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         uint32_t n = 0;  // tiles of P V so far
         for_segments([&](const TreeSeq &sq, int, int, int ta, int nt, int, bool) -> bool {
             if (!wait_all(q_full, n_seg & 1u)) return false;
+            tc_fence_after();
             int ahead = 0;  // tiles of this segment with S issued
             for (; ahead < min(nt, 2); ++ahead) {
                 if (!wait_all(&k_full[kst], kph)) return false;
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t vd = v_desc + (uint64_t)((uint32_t)(st * kTileBytes) >> 4);
-                    const uint32_t tp = tmem + kTmP + (n & 1) * (kBN / 2);
+                    const uint32_t tp = tmem + (C == 1 ? kTmS + (n & 1) * kBN : kTmP);
 #pragma unroll
                     for (int kk = 0; kk < kBN / 16; ++kk)
                         mma_ts(tmem + kTmO, tp + kk * 8, vd + (uint64_t)(kk * 2048 >> 4), id_pv,
@@ -478,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
             for (int k = 0; k < 16; ++k) z[k] = 0u;
 #pragma unroll
-            for (int k = 0; k < kBN / 16; ++k) tmem_st16(trow + kTmP + 16 * k, z);
+            for (int k = 0; k < kBN / 32; ++k) tmem_st16(trow + kTmP + 16 * k, z);
             tmem_wait_st();
         }
         const float2 C2 = make_float2(p.c_log2, p.c_log2);
@@ -491,15 +493,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int i0 = row_token(p, r0), tok = row_tok - i0, h = g * p.G + row - row_tok * p.G;
         const size_t at = (size_t)(sq.row0 + row_tok) * p.s.Hq + h;
         {
-            // Q: this thread's row into the 128-byte-swizzled operand tile (rows that do not exist: zeros)
+            // Q: this thread's row into tensor memory (rows that do not exist: zeros).  From shared memory every S
+            // product read its 16 KB again: 64 sequences of 1 and of 4 tokens 2 to 4 % longer at the power limit, more
+            // tokens 1 %.
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + at * kD);
-            uint4 v[8];
+            uint32_t x[2][16];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = valid ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4 *>(smem + kOffQ + lrow * 128 + ((k ^ (lrow & 7)) << 4)) = v[k];
-            fence_proxy_async_smem();
+            for (int k = 0; k < 8; ++k) {
+                const uint4 v = valid ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                x[k >> 2][4 * (k & 3)] = v.x;
+                x[k >> 2][4 * (k & 3) + 1] = v.y;
+                x[k >> 2][4 * (k & 3) + 2] = v.z;
+                x[k >> 2][4 * (k & 3) + 3] = v.w;
+            }
+            tmem_st16(trow + kTmQ, x[0]);
+            tmem_st16(trow + kTmQ + 16, x[1]);
+            tmem_wait_st();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
@@ -518,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int t = 0; t < nt; ++t, ++n) {
             const int sb = n & 1;
             const int j0 = kfirst + t * kBN;
-            // S(t) is complete, and with it P V(t - 2): this P buffer is free
+            // S(t) is complete, and with it P V(t - 2)
             if (!wait_all(&s_full[sb], (n >> 1) & 1u)) {
                 ok = false;
                 break;
@@ -547,8 +557,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             // P = exp2(S C - m) against the reference, without looking for the tile's maximum: every
             // exponential is at most their sum, and a sum within kSumLimit (NaN fails the test) keeps the
             // reference
+            const uint32_t tp = trow + (C == 1 ? kTmS + sb * kBN : kTmP + copy * (kC / 2));
             float2 acc[2];
-            auto exp_pass = [&](float neg_m) {
+            auto exp_pass = [&](float neg_m) -> bool {
                 const float2 M2 = make_float2(neg_m, neg_m);
                 acc[0] = acc[1] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -561,10 +572,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                         acc[e & 1] = fadd2(acc[e & 1], pe);
                         pk[e] = pack_bf16x2(pe.x, pe.y);
                     }
-                    tmem_st8(trow + kTmP + sb * (kBN / 2) + copy * (kC / 2) + 8 * k, pk);
+                    // one buffer of P: P V(t - 1) must have read it
+                    if (C > 1 && k == 0 && n > 0 && !wait_all(o_done, (n - 1) & 1u)) return false;
+                    tmem_st8(tp + 8 * k, pk);
                 }
+                return true;
             };
-            exp_pass(m == -INFINITY ? 0.f : -m);
+            if (!exp_pass(m == -INFINITY ? 0.f : -m)) {
+                ok = false;
+                break;
+            }
             float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
             const bool big = !(sum <= kSumLimit) || m == -INFINITY;
             if (__any_sync(0xffffffffu, big)) {
@@ -588,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                     if (t > 0) {
                         // O must hold the tile before, too.  (P V(t - 2) is complete, P V(t) not issued:
                         // the parity is unambiguous although other phases go unobserved.)
-                        if (!wait_all(o_done, (n - 1) & 1u)) {
+                        if (C == 1 && !wait_all(o_done, (n - 1) & 1u)) {
                             ok = false;
                             break;
                         }
@@ -664,10 +681,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 }
             }
         } else {
-            // The copies of a row join through Q's buffer, 32 columns at a time (element c of a row at c ^ row:
+            // The copies of a row join through shared memory, 32 columns at a time (element c of a row at c ^ row:
             // no bank conflicts); thread (row, copy) takes the copy-th part of them.  The barriers are
             // reached by all 128 threads, after an expired wait too.
-            float *red = reinterpret_cast<float *>(smem + kOffQ);
+            float *red = reinterpret_cast<float *>(smem + kOffRed);
             float2 *ml = reinterpret_cast<float2 *>(smem + kOffMl);
             if (!ok) *abort_flag = 1;
             ml[lrow] = make_float2(m, l);
