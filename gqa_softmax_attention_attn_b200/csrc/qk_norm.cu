@@ -74,9 +74,9 @@ __device__ __forceinline__ void rotation(const NormParams &p, int pos, int i, fl
 // arrays, a[i] the first halves of pairs 8l + 2i and 8l + 2i + 1 and b[i] their second halves, so that
 // every operation takes two pairs at a time (fp32 x 2 instructions: half the issue slots).
 template <bool kInter>
-__device__ __forceinline__ int chunk0(int l) { return kInter ? 16 * l : 8 * l; }
+__device__ __forceinline__ constexpr int chunk0(int l) { return kInter ? 16 * l : 8 * l; }
 template <bool kInter>
-__device__ __forceinline__ int chunk1(int l) { return kInter ? 16 * l + 8 : kPairs + 8 * l; }
+__device__ __forceinline__ constexpr int chunk1(int l) { return kInter ? 16 * l + 8 : kPairs + 8 * l; }
 
 __device__ __forceinline__ float2 bf2(uint32_t w)
 {
@@ -219,17 +219,21 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const 
     const int hc = live_h ? h : 0;
     const long long tb = (long long)p.T * slab / slabs;
     const int nt = (int)((long long)p.T * (slab + 1) / slabs - tb);  // tokens of the slab
+    // (addresses step by step: products of 64 bits and remainders were a third of the instructions)
     const size_t ss = (size_t)heads * kD;
-    const __nv_bfloat16 *src = p.qkv + tb * ss + hc * kD;
+    const __nv_bfloat16 *src = p.qkv + (tb + tl) * ss + hc * kD + chunk0<kInter>(l);
     const uint32_t ring = smem_u32(ring_raw) + threadIdx.x * 16;
-    auto fetch = [&](int step) {  // the step-th token of this lane
-        const int t = step * kTokLanes + tl;
-        if (t < nt) {
-            const uint32_t dst = ring + (step % kFwdRing) * 2 * kThreads * 16;
-            copy16_async(dst, src + t * ss + chunk0<kInter>(l));
-            copy16_async(dst + kThreads * 16, src + t * ss + chunk1<kInter>(l));
+    int fetched = tl, put = 0, get = 0;  // the lane's next token to fetch; places of the next step in and out
+    auto fetch = [&]() {
+        if (fetched < nt) {
+            const uint32_t dst = ring + put * (2 * kThreads * 16);
+            copy16_async(dst, src);
+            copy16_async(dst + kThreads * 16, src + (chunk1<kInter>(0) - chunk0<kInter>(0)));
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        fetched += kTokLanes;
+        src += kTokLanes * ss;
+        put = put + 1 == kFwdRing ? 0 : put + 1;
     };
     auto rotations = [&](int t0) {  // of tokens [t0, t0 + kBTok) of the slab
         for (int a = threadIdx.x; a < kBTok * kPairs; a += kThreads)
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const 
                 rotation(p, p.pos[tb + t0 + a / kPairs], a % kPairs, rot[t0 / kBTok & 1][a / kPairs]);
     };
 #pragma unroll
-    for (int s = 0; s < kFwdRing - 1; ++s) fetch(s);
+    for (int s = 0; s < kFwdRing - 1; ++s) fetch();
     float2 ba[4], bb[4], wa[4], wb[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) ba[j] = bb[j] = make_float2(0.f, 0.f);
@@ -247,23 +251,23 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const 
     // where its rows go: q by token, k and v by cache row
     const bool is_q = h < p.Hq;
     __nv_bfloat16 *out = is_q ? q + h * kD : h < p.Hq + p.Hkv ? k + (h - p.Hq) * kD : v + (h - p.Hq - p.Hkv) * kD;
-    const size_t stride = (size_t)(is_q ? p.Hq : p.Hkv) * kD;
-    int step = 0;
+    const unsigned stride = (unsigned)(is_q ? p.Hq : p.Hkv) * kD;
     for (int t0 = 0; t0 < nt; t0 += kBTok) {
         __syncthreads();  // this batch's rotations are there, and the other buffer's readers done
         if (t0 + kBTok < nt) rotations(t0 + kBTok);
         const int n = min(kBTok, nt - t0);
 #pragma unroll 1
-        for (int x = 0; x < n; x += kTokLanes, ++step) {  // (the shuffles need whole warps: no lane leaves)
+        for (int x = 0; x < n; x += kTokLanes) {  // (the shuffles need whole warps: no lane leaves)
             const int tt = x + tl;
             const bool live = live_h && tt < n;
-            const long long t = tb + t0 + tt;
-            const long long row = !is_q && p.kv_rows && live ? p.kv_rows[t] : t;
+            const int t = (int)tb + t0 + tt;
+            const int row = !is_q && p.kv_rows && live ? p.kv_rows[t] : t;
             asm volatile("cp.async.wait_group %0;" ::"n"(kFwdRing - 2) : "memory");
-            const uint4 *mine = reinterpret_cast<const uint4 *>(ring_raw) + (step % kFwdRing) * 2 * kThreads + threadIdx.x;
+            const uint4 *mine = reinterpret_cast<const uint4 *>(ring_raw) + get * (2 * kThreads) + threadIdx.x;
+            get = get + 1 == kFwdRing ? 0 : get + 1;
             float2 a[4], b[4];
             unpack<kInter>(mine[0], mine[kThreads], a, b);
-            fetch(step + kFwdRing - 1);  // into the step before's place
+            fetch();  // into the step before's place
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 a[j] = fadd2(a[j], ba[j]);
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const 
                 }
             }
             if (live && (is_q || (row >= 0 && row < p.kv_rows_total))) {
-                __nv_bfloat16 *dst = out + row * stride;
+                __nv_bfloat16 *dst = out + (size_t)(unsigned)row * stride;
                 uint4 o0, o1;
                 pack<kInter>(a, b, o0, o1);
                 *reinterpret_cast<uint4 *>(dst + chunk0<kInter>(l)) = o0;
@@ -318,50 +322,56 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) qk_norm_bwd_kernel(const 
     const long long tb = (long long)p.T * slab / bp.slabs, te = (long long)p.T * (slab + 1) / bp.slabs;
     const int nt = (int)(te - tb);  // tokens of the slab
     // this thread's rows: token tb + tl of the inputs and of the gradient of its head, and their strides
-    const __nv_bfloat16 *src = p.qkv + ((size_t)tb * heads + hc) * kD;
+    const __nv_bfloat16 *src = p.qkv + ((size_t)(tb + tl) * heads + hc) * kD + chunk0<kInter>(l);
     const size_t gs = is_q || !live_h ? (size_t)p.Hq * kD : (size_t)p.Hkv * kD, ss = (size_t)heads * kD;
     const __nv_bfloat16 *gsrc = (is_q || !live_h ? bp.dq + (live_h ? h : 0) * kD
                                  : rotated       ? bp.dk + (h - p.Hq) * kD
-                                                 : bp.dv + (h - p.Hq - p.Hkv) * kD) + tb * gs;
+                                                 : bp.dv + (h - p.Hq - p.Hkv) * kD) + (tb + tl) * gs + chunk0<kInter>(l);
+    constexpr int kOther = chunk1<kInter>(0) - chunk0<kInter>(0);  // from a lane's first chunk to its second
     const uint32_t ring = smem_u32(ring_raw) + threadIdx.x * 16;
-    auto fetch = [&](int step) {  // the step-th token of this lane
-        const int t = step * kTokLanes + tl;
-        if (t < nt) {
-            const uint32_t dst = ring + (step % kRing) * 4 * kThreads * 16;
-            copy16_async(dst, src + t * ss + chunk0<kInter>(l));
-            copy16_async(dst + kThreads * 16, src + t * ss + chunk1<kInter>(l));
-            copy16_async(dst + 2 * kThreads * 16, gsrc + t * gs + chunk0<kInter>(l));
-            copy16_async(dst + 3 * kThreads * 16, gsrc + t * gs + chunk1<kInter>(l));
+    int fetched = tl, put = 0, get = 0;  // the lane's next token to fetch; places of the next step in and out
+    auto fetch = [&]() {
+        if (fetched < nt) {
+            const uint32_t dst = ring + put * (4 * kThreads * 16);
+            copy16_async(dst, src);
+            copy16_async(dst + kThreads * 16, src + kOther);
+            copy16_async(dst + 2 * kThreads * 16, gsrc);
+            copy16_async(dst + 3 * kThreads * 16, gsrc + kOther);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        fetched += kTokLanes;
+        src += kTokLanes * ss;
+        gsrc += kTokLanes * gs;
+        put = put + 1 == kRing ? 0 : put + 1;
     };
+    __nv_bfloat16 *dst = bp.dqkv + ((size_t)(tb + tl) * heads + hc) * kD + chunk0<kInter>(l);
     auto rotations = [&](int t0) {  // of tokens [t0, t0 + kBTok) of the slab
         for (int a = threadIdx.x; a < kBTok * kPairs; a += kThreads)
             if (t0 + a / kPairs < nt)
                 rotation(p, p.pos[tb + t0 + a / kPairs], a % kPairs, rot[t0 / kBTok & 1][a / kPairs]);
     };
 #pragma unroll
-    for (int s = 0; s < kRing - 1; ++s) fetch(s);
+    for (int s = 0; s < kRing - 1; ++s) fetch();
     float2 ba[4], bb[4], wa[4], wb[4], sa[4], sb[4], ga[4], gb[4];  // bias, weight, dbias sums, weight sums
 #pragma unroll
     for (int j = 0; j < 4; ++j) ba[j] = bb[j] = sa[j] = sb[j] = ga[j] = gb[j] = make_float2(0.f, 0.f);
     if (p.bias) load_pairs<kInter>(p.bias + hc * kD, l, ba, bb);
     load_pairs<kInter>(is_q ? p.qw : p.kw, l, wa, wb);
     rotations(0);
-    int step = 0;
     for (int t0 = 0; t0 < nt; t0 += kBTok) {
         __syncthreads();  // this batch's rotations are there, and the other buffer's readers done
         if (t0 + kBTok < nt) rotations(t0 + kBTok);
 #pragma unroll 1
-        for (int x = 0; x < min(kBTok, nt - t0); x += kTokLanes, ++step) {
+        for (int x = 0; x < min(kBTok, nt - t0); x += kTokLanes, dst += kTokLanes * ss) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
             const int tt = x + tl;
             const bool live = live_h && t0 + tt < nt;
-            const uint4 *mine = reinterpret_cast<const uint4 *>(ring_raw) + (step % kRing) * 4 * kThreads + threadIdx.x;
+            const uint4 *mine = reinterpret_cast<const uint4 *>(ring_raw) + get * (4 * kThreads) + threadIdx.x;
+            get = get + 1 == kRing ? 0 : get + 1;
             float2 a[4], b[4], ua[4], ub[4];
             unpack<kInter>(mine[0], mine[kThreads], a, b);
             unpack<kInter>(mine[2 * kThreads], mine[3 * kThreads], ua, ub);
-            fetch(step + kRing - 1);  // into the step before's place
+            fetch();  // into the step before's place
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 a[j] = fadd2(a[j], ba[j]);
@@ -401,9 +411,8 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) qk_norm_bwd_kernel(const 
                 }
                 uint4 c0, c1;
                 pack<kInter>(ua, ub, c0, c1);
-                __nv_bfloat16 *dst = bp.dqkv + ((size_t)(tb + t0 + tt) * heads + h) * kD;
-                *reinterpret_cast<uint4 *>(dst + chunk0<kInter>(l)) = c0;
-                *reinterpret_cast<uint4 *>(dst + chunk1<kInter>(l)) = c1;
+                *reinterpret_cast<uint4 *>(dst) = c0;
+                *reinterpret_cast<uint4 *>(dst + kOther) = c1;
             }
         }
     }
