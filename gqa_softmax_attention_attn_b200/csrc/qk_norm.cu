@@ -17,13 +17,13 @@
 // rotation needs no exchange and a sum over the head is two shuffles.
 //
 // Bound by HBM and instruction issue together (64 + 8 + 8 heads): forward of
-// 4096 tokens 17.3 us, 4.8 TB/s; of 16384 tokens 63 us under a profiler, 4.6 TB/s
-// of DRAM with 60 % of the issue slots taken; backward of 65536 tokens 359 us, 5.6 TB/s (406
-// in runs of seconds, at the power limit, the clock down to 1.73 GHz); of 1003
+// 4096 tokens 16.6 us, 5.1 TB/s; backward of 65536 tokens 340 us, 5.9 TB/s (361 to 374
+// in runs of seconds, at the power limit, the clock down to 1.7 to 1.8 GHz); of 1003
 // tokens 10.8 us, two launches and the latency of one slab.  Two pairs per
 // instruction, the asynchronous ring and slabs as many as run at once brought
-// 4096 tokens from 26.6 us and 65536 tokens backward from 614 us; starting while
-// the grid ahead ends took 512 tokens from 4.5 to 4.1 us.
+// 4096 tokens from 26.6 us and 65536 tokens backward from 614 us, addresses step by
+// step the last 4 and 6 %; starting while
+// the grid ahead ends took 512 tokens from 4.5 to 4.1 us, now 3.9.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const 
     const int hc = live_h ? h : 0;
     const long long tb = (long long)p.T * slab / slabs;
     const int nt = (int)((long long)p.T * (slab + 1) / slabs - tb);  // tokens of the slab
-    // (addresses step by step: products of 64 bits and remainders were a third of the instructions)
+    // (addresses step by step: with products of 64 bits and remainders 4096 tokens took 17.3 us instead of 16.6)
     const size_t ss = (size_t)heads * kD;
     const __nv_bfloat16 *src = p.qkv + (tb + tl) * ss + hc * kD + chunk0<kInter>(l);
     const uint32_t ring = smem_u32(ring_raw) + threadIdx.x * 16;
