@@ -25,9 +25,18 @@ __device__ __forceinline__ void tree_paths(const TreeShape &s, const TreeSeq &q,
     sync();
     for (int k = tid; k < n; k += nthreads) {
         for (int w = 0; w < kPathWords; ++w) bits[k][w] = 0u;
-        int d = 0;
-        for (int a = i0 + k; a >= 0; a = par[a], ++d)
-            if (s.window <= 0 || d < s.window) bits[k][a >> 5] |= 1u << (a & 31);
+        // the walk meets the words of the row from the last to the first: each is gathered in a register
+        int d = 0, w = (i0 + k) >> 5;
+        uint32_t word = 0u;
+        for (int a = i0 + k; a >= 0; a = par[a], ++d) {
+            if (a >> 5 != w) {
+                bits[k][w] = word;
+                word = 0u;
+                w = a >> 5;
+            }
+            if (s.window <= 0 || d < s.window) word |= 1u << (a & 31);
+        }
+        bits[k][w] = word;
         depth[k] = (int16_t)(d - 1);
     }
     sync();

@@ -15,7 +15,7 @@
 // exp2f.  Where rows are many, bound by shared-memory reads (a read of K and a
 // broadcast of q per FMA of the scores); where they are few, by the latency of
 // a tile's chain, so the keys are cut into chunks of a single tile if need be
-// to put sixteen CTAs on an SM (3 sequences of 7 tokens: 21 us a call on the
+// to put sixteen CTAs on an SM (3 sequences of 7 tokens: 19 us a call on the
 // device, 60 us a call in chunks of 16 tiles).
 #include <cuda_bf16.h>
 #include <math.h>
