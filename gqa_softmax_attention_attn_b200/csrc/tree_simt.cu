@@ -16,7 +16,7 @@
 // 608 -> 412 us).  Where rows are many, bound by FMA issue and
 // the exchange of the weights (a shuffle per two FMAs); where they are few, by the latency of
 // a tile's chain, so the keys are cut into chunks of a single tile if need be
-// to put sixteen CTAs on an SM (3 sequences of 7 tokens: 14 us a call on the
+// to put sixteen CTAs on an SM (3 sequences of 7 tokens: 13.5 us a call on the
 // device, 60 us a call in chunks of 16 tiles).
 #include <cuda_bf16.h>
 #include <math.h>
@@ -76,6 +76,18 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
     const int nrow = min(kRows, rows - r0);
     const int kbeg = max(sq.lo, sq.lo_al + c * s.chunk), kend = min(sq.len, sq.lo_al + (c + 1) * s.chunk);
 
+    // a tile's K and V, a quarter of a key's row a thread, loaded a tile ahead (the first beside the paths and q)
+    const int jj0 = tid >> 2, d0 = (tid & 3) * 16;
+    float4 kv[4], vv[4];
+    auto load = [&](int j0) {
+        const long long at = j0 + jj0 < kend ? kv_offset(s, b, j0 + jj0, g) : -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            kv[e] = at >= 0 ? *reinterpret_cast<const float4 *>(kc + at + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+            vv[e] = at >= 0 ? *reinterpret_cast<const float4 *>(vc + at + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    load(kbeg);
     const int i0 = r0 / G, ntok = (r0 + nrow - 1) / G - i0 + 1;
     tree_paths(s, sq, i0, ntok, tid, 128, par, path, depth, [] { __syncthreads(); });
     for (int e = tid; e < nrow * kD; e += 128) {
@@ -96,27 +108,17 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
     const float C = s.scale * kLog2e;
     for (int j0 = kbeg; j0 < kend; j0 += 32) {
         __syncthreads();
-        {
-            // a quarter of a key's row a thread
-            const int jj = tid >> 2, d0 = (tid & 3) * 16;
-            const long long at = j0 + jj < kend ? kv_offset(s, b, j0 + jj, g) : -1;
-            float4 kv[4], vv[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                kv[e] = at >= 0 ? *reinterpret_cast<const float4 *>(kc + at + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
-                vv[e] = at >= 0 ? *reinterpret_cast<const float4 *>(vc + at + d0 + 4 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float *k = &ks[jj][d0 + 4 * e];
-                k[0] = kv[e].x;
-                k[1] = kv[e].y;
-                k[2] = kv[e].z;
-                k[3] = kv[e].w;
-                *reinterpret_cast<float4 *>(&vs[jj][d0 + 4 * e]) = vv[e];
-            }
+        for (int e = 0; e < 4; ++e) {
+            float *k = &ks[jj0][d0 + 4 * e];
+            k[0] = kv[e].x;
+            k[1] = kv[e].y;
+            k[2] = kv[e].z;
+            k[3] = kv[e].w;
+            *reinterpret_cast<float4 *>(&vs[jj0][d0 + 4 * e]) = vv[e];
         }
         __syncthreads();
+        if (j0 + 32 < kend) load(j0 + 32);
         // the warp's four rows side by side (rows that do not exist are computed and not stored): each K and V
         // value is read once for them, and their reductions overlap
         const int j = j0 + lane, a = j - sq.cached;
