@@ -1,11 +1,12 @@
-"""The QK-norm backward in its steady state: slabs of several batches of rotations and many turns of the ring, and
-the gradients summed over tokens held to the depth of the kernel's own sums."""
+"""The QK-norm prologue and its backward in their steady state: slabs of several batches of rotations and many
+turns of the rings, and the gradients summed over tokens held to the depth of the kernel's own sums."""
 import numpy as np
 import pytest
 import torch
 
+import gqa_softmax_attention_attn_b200 as attn
 import oracle
-from test_qk_norm import D, EPS, YARN, close, make, oracle_rope, run_bwd, up
+from test_qk_norm import D, EPS, YARN, close, forward_bound, make, oracle_rope, run_bwd, up
 
 gpu = pytest.mark.gpu
 # (tokens, query heads, KV heads): 46 or 47 tokens a slab forward, 69 to 72 backward, the last steps and batches
@@ -108,3 +109,38 @@ def test_backward_many_batches_a_slab(T, Hq, Hkv, interleaved):
     E = r * (wA + n * (wA * n).mean(-1, keepdims=True))
     E = 2.0 ** -18 * np.concatenate([E, np.zeros((T, Hkv, D))], 1).reshape(T, -1)
     close(dqkv, s.dx, E + 2.0 ** -8 * (np.abs(s.dx) + E) + 1e-30, "dqkv")
+
+
+@gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,Hq,Hkv", SHAPES)
+def test_forward_many_batches_a_slab(T, Hq, Hkv, interleaved):
+    """In token order, and into a cache whose rows are taken in random order, every eighth token without one."""
+    c = make(T, Hq, Hkv, 82)
+    t = up(c)
+    rq, rk, rv = oracle.qk_norm_prologue(c["qkv"], c["bias"], c["qw"], c["kw"], c["pos"], Hq, Hkv, D, EPS,
+                                         interleaved=interleaved, **oracle_rope(YARN))
+    kb, vb = forward_bound(c, rk, Hq, Hkv, c["kw"]), 2.0 ** -8 * np.abs(rv) + 2.0 ** -20
+    qb = forward_bound(c, rq, Hq, Hkv, c["qw"])
+    total = 2 * T + 5
+    rows = torch.randperm(total, generator=torch.Generator().manual_seed(7))[:T]
+    rows[::8] = -1
+    kept = [i for i in range(T) if i % 8]
+    for cache in (False, True):
+        n = total if cache else T
+        q = torch.full((T, Hq, D), 5.0, dtype=torch.bfloat16, device="cuda")
+        k, v = (torch.full((n, Hkv, D), 5.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        attn.attn_sink_qk_norm_prologue(t["qkv"], t["bias"], t["qw"], t["kw"], t["pos"], q, k, v, EPS,
+                                        interleaved=interleaved, kv_rows=rows.int().cuda() if cache else None, **YARN)
+        torch.cuda.synchronize()
+        close(q, rq, qb, "q")
+        if not cache:
+            close(k, rk, kb, "k")
+            close(v, rv, vb, "v")
+            continue
+        at = rows[kept].cuda()
+        close(k[at], rk[kept], kb[kept], "k")
+        close(v[at], rv[kept], vb[kept], "v")
+        rest = torch.ones(n, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert (k[rest] == 5.0).all() and (v[rest] == 5.0).all()
