@@ -675,9 +675,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The backward's last step, one launch: blocks [0, n_conv) turn the fp32 dQ
 // accumulator into bf16 (8 values per thread); block n_conv + h sums head h's
 // B * Lq dsink terms in a fixed order (deterministic).
-__global__ void __launch_bounds__(256) bwd_finish_kernel(const float *__restrict__ acc, __nv_bfloat16 *__restrict__ dq,
-                                                         size_t n8, unsigned n_conv, const float *__restrict__ terms,
-                                                         float *__restrict__ dsinks, long nterms)
+__global__ void __launch_bounds__(256) bwd_finish_kernel(const float *acc, __nv_bfloat16 *dq, size_t n8,
+                                                         unsigned n_conv, const float *terms, float *dsinks,
+                                                         long nterms)
 {
     grid_dep_wait();  // launched ahead of the main kernel's end: its dQ and the pre-pass's terms
     if (blockIdx.x >= n_conv) {

@@ -197,7 +197,9 @@ double rope_attention_factor(const RopeParams &r);
 
 // Launches kern as the dependent of the grid ahead on the stream (programmatic dependent launch): it may start
 // while that grid still runs, once all of its CTAs have started and allowed it, and touches global memory only
-// behind its own grid_dep_wait(), which every one of its threads reaches first.
+// behind its own grid_dep_wait(), which every one of its threads reaches first.  Its pointers are not __restrict__:
+// the grid ahead writes what they point at during this kernel's own life, and a load that the compiler takes for one of
+// memory that nobody writes may be moved in front of the wait, or go through a cache that the wait does not refresh.
 template <typename... P, typename... A>
 cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A... args)
 {

@@ -32,9 +32,8 @@ constexpr int kTokens = 256;              // tokens per CTA
 
 struct MapParams {
     PageMapShape s;
-    const int *__restrict__ cached, *__restrict__ fresh, *__restrict__ parents, *__restrict__ free_pages;
-    int *page_table, *__restrict__ seqlens, *__restrict__ cu, *__restrict__ positions, *__restrict__ rows,
-        *__restrict__ stats;
+    const int *cached, *fresh, *parents, *free_pages;
+    int *page_table, *seqlens, *cu, *positions, *rows, *stats;
 };
 
 struct Request {

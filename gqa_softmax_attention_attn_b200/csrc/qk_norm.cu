@@ -38,10 +38,10 @@ constexpr int kPairs = kD / 2;
 constexpr int kThreads = 256;
 
 struct NormParams {
-    const __nv_bfloat16 *__restrict__ qkv;
-    const float *__restrict__ bias;  // [(Hq + 2 Hkv) * D] or nullptr
-    const float *__restrict__ qw, *__restrict__ kw;
-    const int *__restrict__ pos, *__restrict__ kv_rows;
+    const __nv_bfloat16 *qkv;
+    const float *bias;  // [(Hq + 2 Hkv) * D] or nullptr
+    const float *qw, *kw;
+    const int *pos, *kv_rows;
     float eps;
     int T, Hq, Hkv, kv_rows_total;
     float attn_factor;
@@ -50,10 +50,10 @@ struct NormParams {
 
 struct BwdParams {
     NormParams n;
-    const __nv_bfloat16 *__restrict__ dq, *__restrict__ dk, *__restrict__ dv;
-    __nv_bfloat16 *__restrict__ dqkv;
-    float *__restrict__ dbias, *__restrict__ dqw, *__restrict__ dkw;
-    float *__restrict__ ws;
+    const __nv_bfloat16 *dq, *dk, *dv;
+    __nv_bfloat16 *dqkv;
+    float *dbias, *dqw, *dkw;
+    float *ws;
     int slabs, groups;
 };
 
@@ -203,9 +203,8 @@ constexpr int kFwdRing = 4, kFwdPerSm = 3;
 
 template <bool kInter>
 __global__ void __launch_bounds__(kThreads, kFwdPerSm) qk_norm_fwd_kernel(const NormParams p, int slabs,
-                                                                          __nv_bfloat16 *__restrict__ q,
-                                                                          __nv_bfloat16 *__restrict__ k,
-                                                                          __nv_bfloat16 *__restrict__ v)
+                                                                          __nv_bfloat16 *q, __nv_bfloat16 *k,
+                                                                          __nv_bfloat16 *v)
 {
     grid_dep_launch();
     grid_dep_wait();  // the grid ahead

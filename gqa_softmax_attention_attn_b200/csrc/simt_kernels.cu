@@ -515,11 +515,9 @@ __global__ void __launch_bounds__(128) decode_simt_kernel(const T *__restrict__ 
 // One warp per (b, h): M = max(sink, max_c m_c), L = 2^(sink-M) + sum_c l_c 2^(m_c-M),
 // o = sum_c 2^(m_c-M) o_c / L, lse = (M + log2 L) ln 2.  The sink enters once.
 template <typename T>
-__global__ void __launch_bounds__(128) decode_combine_kernel(const int *__restrict__ seqlens,
-                                                             const float *__restrict__ sinks, T *__restrict__ out,
-                                                             float *__restrict__ lse,
-                                                             const float *__restrict__ ws_o,
-                                                             const float *__restrict__ ws_ml, DecodeShape s)
+__global__ void __launch_bounds__(128) decode_combine_kernel(const int *seqlens, const float *sinks, T *out,
+                                                             float *lse, const float *ws_o, const float *ws_ml,
+                                                             DecodeShape s)
 {
     grid_dep_wait();  // the split partials of the decode grid ahead (programmatic dependent launch)
     const int lane = threadIdx.x & 31;

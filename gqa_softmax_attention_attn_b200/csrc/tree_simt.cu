@@ -53,10 +53,9 @@ __device__ __forceinline__ long long kv_offset(const TreeShape &s, int b, int j,
     return (((long long)page * s.page_size + j % s.page_size) * s.Hkv + g) * kD;
 }
 
-__global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict__ q, const float *__restrict__ kc,
-                                                        const float *__restrict__ vc, float *__restrict__ out,
-                                                        float *__restrict__ lse, float *__restrict__ ws_o,
-                                                        float *__restrict__ ws_ml, const TreeShape s, int row_tiles)
+__global__ void __launch_bounds__(128) tree_simt_kernel(const float *q, const float *kc, const float *vc, float *out,
+                                                        float *lse, float *ws_o, float *ws_ml, const TreeShape s,
+                                                        int row_tiles)
 {
     grid_dep_launch();  // the combine may start its set-up; it waits for this grid
     grid_dep_wait();    // (as this one for the grid ahead)
@@ -189,9 +188,8 @@ __global__ void __launch_bounds__(128) tree_simt_kernel(const float *__restrict_
 // One warp per (token, query head): M = max(sink, max_c m_c), L = 2^(sink - M)
 // + sum_c l_c 2^(m_c - M), o = sum_c 2^(m_c - M) o_c / L, the splits in order
 // (so the result does not depend on which finished first).
-__global__ void __launch_bounds__(128) tree_combine_kernel(float *__restrict__ out, float *__restrict__ lse,
-                                                           const float *__restrict__ ws_o,
-                                                           const float *__restrict__ ws_ml, const TreeShape s)
+__global__ void __launch_bounds__(128) tree_combine_kernel(float *out, float *lse, const float *ws_o,
+                                                           const float *ws_ml, const TreeShape s)
 {
     grid_dep_wait();  // the partials of the grid ahead (programmatic dependent launch)
     const TreeSeq sq = tree_seq(s, blockIdx.y);
