@@ -191,7 +191,7 @@ TreeShape tree_shape(int B, int total_q, int max_q, int Lmax, int Hq, int Hkv, i
     // keys from the first one a root sees, rounded down to a tile, to the last drafted one
     const long long lw = window > 0 ? (long long)window - 1 + max_q + kTreeTile - 1 : (long long)Lmax;
     const long long lvis = lw < Lmax ? lw : Lmax;
-    // (automatic: some sixteen CTAs an SM, each at least a tile of keys)
+    // (automatic: some sixteen CTAs an SM -- four at a time -- each at least a tile of keys)
     long long splits = num_splits > 0 ? num_splits : 16 * 148 / ctas;
     splits = splits < 1 ? 1 : (splits > kTreeMaxSplits ? kTreeMaxSplits : splits);
     long long chunk = (lvis + splits - 1) / splits;

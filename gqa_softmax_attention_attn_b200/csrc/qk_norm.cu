@@ -17,9 +17,9 @@
 // rotation needs no exchange and a sum over the head is two shuffles.
 //
 // Bound by HBM and instruction issue together (64 + 8 + 8 heads): forward of
-// 4096 tokens 16.6 us, 5.1 TB/s; backward of 65536 tokens 340 us, 5.9 TB/s (361 to 374
+// 4096 tokens 16.0 to 16.6 us, 5.1 TB/s; backward of 65536 tokens 340 to 346 us, 5.9 TB/s (359 to 378
 // in runs of seconds, at the power limit, the clock down to 1.7 to 1.8 GHz); of 1003
-// tokens 10.8 us, two launches and the latency of one slab.  Two pairs per
+// tokens 10.8 to 11.4 us, two launches and the latency of one slab.  Two pairs per
 // instruction, the asynchronous ring and slabs as many as run at once brought
 // 4096 tokens from 26.6 us and 65536 tokens backward from 614 us, addresses step by
 // step the last 4 and 6 %; starting while

@@ -12,12 +12,15 @@
 // CTA = (16 rows of one KV head, split, sequence): keys in tiles of 32, lane =
 // key for the scores and lane = (d, d + 32) for the output, so that K and V
 // are read once for 16 rows.  Every score and sum is fp32, each exponential
-// exp2f.  A warp's four rows go side by side (16 sequences of 61 tokens
-// 608 -> 412 us).  Where rows are many, bound by FMA issue and
-// the exchange of the weights (a shuffle per two FMAs); where they are few, by the latency of
+// exp2f.  A warp's four rows go side by side (16 sequences of 61 tokens, 6 query and
+// 2 KV heads, 2000 to 4000 keys: 608 -> 412 us, 11 TFLOP/s; with 64 and 8 heads 3924 us,
+// 12 TFLOP/s, against 74 at two flop a lane and cycle).  Where rows are many, bound by issue:
+// the products of Q K^T feed on shared memory, and two FMAs of P V bring a shuffle
+// and two selects with them.  Where they are few, bound by the latency of
 // a tile's chain, so the keys are cut into chunks of a single tile if need be
-// to put sixteen CTAs on an SM (3 sequences of 7 tokens: 13.5 us a call on the
-// device, 60 us a call in chunks of 16 tiles).
+// until there are sixteen CTAs an SM, of which it runs four at a time (128 registers a
+// thread): 3 sequences of 7 tokens 12.3 us a call on the
+// device, 60 us a call in chunks of 16 tiles.
 #include <cuda_bf16.h>
 #include <math.h>
 

@@ -10,7 +10,7 @@
 // of bf16, is what reaches the output) and the row sum adds the unrounded P.
 //
 // Design: T drafted tokens times G query heads of a KV group share every K/V
-// byte, T G 64 flop a byte: with up to 128 rows a KV head the kernel is bound by
+// byte, T G 64 flop a byte: with up to 64 rows a KV head the kernel is bound by
 // HBM, beyond that by the softmax (one exponential per 256 flop).
 //  * The work is one line of 64-key tiles, sequence by sequence, cut evenly over
 //    teams of CTAs, whatever the lengths: as many as fit the GPU at once (two CTAs
@@ -50,15 +50,22 @@
 //    scores are selected away, their V rows zeroed in shared memory.
 //  * Every wait is bounded; on expiry the CTA raises the device status bit, waits
 //    (bounded) for its own loads and MMAs, frees tensor memory and exits.
+//  * The host divides the GPU for max_q tokens in every sequence: a CTA whose row tile
+//    a sequence does not reach skips it, so a bound above the drafts, or one long draft among
+//    short ones, leaves that part of the GPU idle (64 sequences of 8 tokens 404 us with a bound
+//    of 8, 850 with 32, 5912 with 256).
 // Measured (64 query and 8 KV heads): 64 sequences of 1024 to 32768 keys in pages of
-// 16, 8 tokens each, 370 to 395 us, 5.6 to 6.0 TB/s, bound by HBM in short runs.  Repeated
+// 16, 8 tokens each, 370 to 407 us, 5.5 to 6.0 TB/s, bound by HBM in short runs.  Repeated
 // for seconds it takes 425 to 475 us: HBM, the products and the exponentials
 // together reach the 1000 W limit and the clock falls to 1.2 to 1.4 GHz (without
 // the products 360 us).  Beyond 64 rows a KV head the softmax warps' chain
-// bounds it: 16 sequences of 61 tokens 202 us, one of 131072 keys with 32 tokens 119
-// us; a tile is 1500 cycles of it, 880 in the pass of the exponentials (two CTAs'
+// bounds it: 16 sequences of 61 tokens 202 to 211 us, one of 131072 keys with 32 tokens 119 to 130
+// us; a tile is 1500 to 1650 cycles of it, 880 in the pass of the exponentials (two CTAs'
 // warps share a scheduler; 440 without the exponentials) and 600 in its waits, votes,
-// loads and arrivals, 90 to 180 each.  (Not bounded by the S products: with three S buffers
+// loads and arrivals, 90 to 180 each.  Of the 318000 cycles of a CTA of the first, 182 us at the
+// 1.7 to 1.8 GHz that it runs at, 282000 are its 172 tiles, 9000 epilogues, 5000 the plan, 1000
+// first scores and 20000 the segments' starts (Q, paths) and end; of 200000 of the second (116 us)
+// 184000 are its 114 tiles.  (Not bounded by the S products: with three S buffers
 // 201 us; nor by the load of S: with the next tile's scores loaded during the pass 225 us.)
 #include <cuda.h>
 #include <cuda_bf16.h>
