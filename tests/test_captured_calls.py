@@ -112,3 +112,46 @@ def test_behind_any_node(name):
             for o, w in zip(outs, want):
                 assert torch.equal(o, w), how.__name__
     assert attn.attn_sink_get_device_status() == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("name", CALLS)
+def test_between_two_calls_another_stream_writes(name, captured):
+    """A call whose kernels let the next one in early, then a wait for another stream, whose copy of the input comes
+    late, then the call again: the second reads what the other stream wrote."""
+    src, outs, call = CALLS[name]()
+    call()
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    keep = src.clone()
+    side = torch.cuda.Stream()
+
+    def line():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        call()  # on an input of zeros
+        ready = torch.cuda.Event()
+        ready.record()
+        with torch.cuda.stream(side):
+            side.wait_event(ready)  # (the first call reads the input)
+            torch.cuda._sleep(400000)  # some 200 us
+            src.copy_(keep)
+        call()  # and once more, while the other stream sleeps
+        for o in outs:
+            o.fill_(7)
+        call()
+        here.wait_stream(side)
+        call()
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            line()
+    for _ in range(5):
+        src.zero_()
+        torch.cuda.synchronize()
+        graph.replay() if captured else line()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    assert attn.attn_sink_get_device_status() == 0
